@@ -67,6 +67,9 @@
 #ifndef PA_H_
 #define PA_H_
 
+/* More entry points of the same library, under the same conventions: pa/ops.h
+ * (rotary positions with the cache write, 4-bit pools, sliding windows). */
+
 #include <stddef.h>
 #include <stdint.h>
 

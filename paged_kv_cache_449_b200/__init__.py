@@ -7,6 +7,9 @@ calls raise.  Tensors are torch CUDA tensors; pools are shaped
 element size), so block_size, num_blocks and the head counts are read off the
 tensor shapes.  Calls run on the current torch CUDA stream unless `stream`
 (a torch.cuda.Stream or a raw cudaStream_t int) is given.
+
+The entry points of include/pa/ops.h (rotary positions with the cache write,
+4-bit pools, sliding windows) are in the submodule `ops`, under their C names.
 """
 
 from __future__ import annotations
@@ -27,7 +30,10 @@ __all__ = ["pa_reshape_and_cache", "pa_decode", "pa_decode_append", "pa_decode_s
            "pa_decode_splitk_fp8", "fp8_pool_shape", "pa_prefill", "pa_decode_append_fp8",
            "pa_blocks_init", "pa_blocks_append", "pa_blocks_fork", "pa_blocks_release",
            "DEVERR_NO_FREE_BLOCK", "DEVERR_REF_COUNT", "DEVERR_SHARED_BLOCK", "DEVERR_PREFIX",
-           "pa_decode_shared_prefix", "pa_decode_shared_prefix_workspace_size", "prepare_decode_shared_prefix"]
+           "pa_decode_shared_prefix", "pa_decode_shared_prefix_workspace_size", "prepare_decode_shared_prefix",
+           "prepare_rope_and_cache", "prepare_reshape_and_cache_int4", "prepare_gather_cache_int4",
+           "prepare_decode_int4", "prepare_decode_window", "prepare_prefill_window", "rope_frequencies",
+           "int4_pool_shape", "ops"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libpa.so")
@@ -65,7 +71,7 @@ def load() -> ctypes.CDLL:
 
 def load_library(path: str) -> ctypes.CDLL:
     """Open a build of the library at `path` with the argument types of every
-    entry point declared in include/pa.h."""
+    entry point declared in include/pa.h and include/pa/ops.h."""
     lib = ctypes.CDLL(path)
     c = ctypes
     P, I, I64, F, SZ = c.c_void_p, c.c_int, c.c_int64, c.c_float, c.c_size_t
@@ -107,6 +113,28 @@ def load_library(path: str) -> ctypes.CDLL:
     lib.pa_blocks_fork.argtypes = [P, P, P, P, I, I, I, I, I64, P]
     lib.pa_blocks_release.restype = I
     lib.pa_blocks_release.argtypes = [P, P, P, P, P, P, I, I, I, I, I64, P]
+    rope_args = [P, P, P, P, P, P, P, P, P, P, P, F, F, I, I, I64, I64, I64, I64, I, I, I, I, I64, I, P]
+    for name in ("pa_rope_and_cache", "pa_rope_and_cache_int4"):
+        getattr(lib, name).restype = I
+        getattr(lib, name).argtypes = rope_args
+    lib.pa_rope_and_cache_fp8.restype = I
+    lib.pa_rope_and_cache_fp8.argtypes = rope_args[:6] + [P, P] + rope_args[6:]
+    for name in ("pa_reshape_and_cache_int4", "pa_gather_cache_int4"):
+        getattr(lib, name).restype = I
+        getattr(lib, name).argtypes = [P, P, P, P, P, I64, I, I, I, I64, I, P]
+    lib.pa_decode_window_plan.restype = I
+    lib.pa_decode_window_plan.argtypes = [I, I, I, I, I, I, I, I, c.POINTER(I), c.POINTER(SZ)]
+    lib.pa_decode_int4_plan.restype = I
+    lib.pa_decode_int4_plan.argtypes = [I, I, I, I, I, I, I, c.POINTER(I), c.POINTER(SZ)]
+    split_args = [I, I, I, P, SZ, P, I64]
+    lib.pa_decode_window.restype = I
+    lib.pa_decode_window.argtypes = [P, P, P, P] + decode_args[2:] + split_args + [P, P, P]
+    lib.pa_decode_window_fp8.restype = I
+    lib.pa_decode_window_fp8.argtypes = [P, P, P, P] + fp8_args[2:] + split_args + [P, P, P]
+    lib.pa_decode_int4.restype = I
+    lib.pa_decode_int4.argtypes = decode_args + split_args + [P, P]
+    lib.pa_prefill_window.restype = I
+    lib.pa_prefill_window.argtypes = lib.pa_prefill.argtypes[:-1] + [I, I, P]
     lib.pa_get_device_error.restype = I
     lib.pa_get_device_error.argtypes = [P, c.POINTER(c.c_int32)]
     lib.pa_status_string.restype = c.c_char_p
@@ -453,13 +481,25 @@ def _accessible_ptr(t: torch.Tensor, name: str) -> int:
     return t.data_ptr()
 
 
+def _bytes_as_pool(t: torch.Tensor) -> torch.Tensor:
+    """A byte pool [num_blocks, Hkv, ...] as one of 16-bit elements with the
+    same blocks (block size 1, so that a tile is one row of 16-byte vectors)."""
+    if t.dim() not in (3, 5) or not t.is_contiguous():
+        raise ValueError("byte pools are contiguous [num_blocks, Hkv, tile bytes] or [num_blocks, Hkv, D // 16, B, 16]")
+    return t.view(t.shape[0], t.shape[1], -1, 1, 16).view(torch.float16)
+
+
 @_on_tensor_device
 def pa_copy_blocks(dst_k_cache, dst_v_cache, src_k_cache, src_v_cache, block_mapping, stream=None):
     """Copy whole blocks (src, dst) = block_mapping[i] (int64 [n, 2], on the
     device or pinned) from the source pools to the destination pools.  Same
     pools on both sides: copy-on-write duplicates; a pinned CPU pool on one
-    side: swap-out / swap-in.  Pools are [num_blocks, Hkv, D // X, B, X]."""
+    side: swap-out / swap-in.  Pools are [num_blocks, Hkv, D // X, B, X], or the
+    byte pools of the 8- and 4-bit caches."""
     lib = load()
+    if all(t.dtype == torch.uint8 for t in (dst_k_cache, dst_v_cache, src_k_cache, src_v_cache)):
+        dst_k_cache, dst_v_cache, src_k_cache, src_v_cache = (
+            _bytes_as_pool(t) for t in (dst_k_cache, dst_v_cache, src_k_cache, src_v_cache))
     n_src, hkv, d, b = _pool_dims(src_k_cache)
     n_dst, hkv2, d2, b2 = _pool_dims(dst_k_cache)
     if (hkv, d, b) != (hkv2, d2, b2) or src_k_cache.dtype != dst_k_cache.dtype:
@@ -669,3 +709,9 @@ def pa_get_device_error(stream=None) -> int:
     code = ctypes.c_int32(0)
     _check(lib.pa_get_device_error(_stream(stream), ctypes.byref(code)), "pa_get_device_error")
     return int(code.value)
+
+
+from . import ops  # noqa: E402  (it uses the helpers above)
+from .ops import (int4_pool_shape, prepare_decode_int4, prepare_decode_window,  # noqa: E402
+                  prepare_gather_cache_int4, prepare_prefill_window, prepare_reshape_and_cache_int4,
+                  prepare_rope_and_cache, rope_frequencies)

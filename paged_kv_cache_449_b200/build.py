@@ -30,7 +30,7 @@ def nvcc_path() -> str:
 
 def sources() -> list[str]:
     return [SRC] + sorted(glob.glob(os.path.join(HERE, "csrc", "*.cuh"))) + \
-        sorted(glob.glob(os.path.join(ROOT, "include", "*.h")))
+        sorted(glob.glob(os.path.join(ROOT, "include", "**", "*.h"), recursive=True))
 
 
 def build(out: str = LIB, defines: dict | None = None, force: bool = False, verbose: bool = False) -> str:

@@ -18,12 +18,16 @@
 #include <tuple>
 
 #include "pa.h"
+#include "pa/ops.h"
 #include "pa_blocks.cuh"
 #include "pa_copy.cuh"
 #include "pa_decode.cuh"
+#include "pa_decode_int4.cuh"
 #include "pa_prefill.cuh"
 #include "pa_prefill_tc.cuh"
 #include "pa_reshape.cuh"
+#include "pa_rope.cuh"
+#include "pa_rows.cuh"
 
 // Two CTA shapes for the decode kernels, measured on B200 over the benchmark
 // workloads (warps per CTA, shared-memory ring bytes per warp):
@@ -238,12 +242,12 @@ cudaError_t with_variant(pa_dtype dt, int D, int B, F&& f) {
     }
 }
 
-template <typename T, int D, int B, bool SPLIT, Kind K, bool FP8 = false, bool PREFIX = false>
+template <typename T, int D, int B, bool SPLIT, Kind K, bool FP8 = false, bool PREFIX = false, bool WINDOW = false>
 cudaError_t launch_decode(const pa::DecodeParams& p, dim3 grid, cudaStream_t stream) {
     using C = DecodeConfig<T, D, B, K, FP8>;
     auto kernel = pa::pa_decode_kernel<T, D, B, C::kWarps, C::kStages, SPLIT, FP8,
                                        !SPLIT && (!PREFIX || PA_PREFIX_CLASS_EIGHTHS > 0) && K == Kind::kWide,
-                                       PREFIX>;
+                                       PREFIX, WINDOW>;
     cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel));
     if (e != cudaSuccess) return e;
     // The shared-prefix form's CTAs start while the prefix pass (the launch
@@ -270,7 +274,7 @@ int sm_count() {
 
 // The split kernel always runs wide CTAs; the one-pass kernel runs deep CTAs
 // unless its grid holds more than PA_DEEP_MAX_CTAS_PER_SM CTAs per SM.
-template <bool SPLIT, bool FP8 = false, bool PREFIX = false>
+template <bool SPLIT, bool FP8 = false, bool PREFIX = false, bool WINDOW = false>
 cudaError_t decode_dispatch(pa_dtype dt, int D, int B, const pa::DecodeParams& p, dim3 grid, cudaStream_t st) {
     const long long ctas = static_cast<long long>(grid.x) * grid.y * grid.z;
     const bool deep = !SPLIT && ctas <= static_cast<long long>(PA_DEEP_MAX_CTAS_PER_SM) * sm_count();
@@ -283,10 +287,10 @@ cudaError_t decode_dispatch(pa_dtype dt, int D, int B, const pa::DecodeParams& p
             return deep ? launch_decode<T, kD, kB, false, Kind::kDeep, false, true>(p, grid, st)
                         : launch_decode<T, kD, kB, false, Kind::kWide, false, true>(p, grid, st);
         } else if constexpr (SPLIT) {
-            return launch_decode<T, kD, kB, true, Kind::kWide, FP8>(p, grid, st);
+            return launch_decode<T, kD, kB, true, Kind::kWide, FP8, false, WINDOW>(p, grid, st);
         } else {
-            return deep ? launch_decode<T, kD, kB, false, Kind::kDeep, FP8>(p, grid, st)
-                        : launch_decode<T, kD, kB, false, Kind::kWide, FP8>(p, grid, st);
+            return deep ? launch_decode<T, kD, kB, false, Kind::kDeep, FP8, false, WINDOW>(p, grid, st)
+                        : launch_decode<T, kD, kB, false, Kind::kWide, FP8, false, WINDOW>(p, grid, st);
         }
     });
 }
@@ -469,11 +473,11 @@ constexpr int prefill_tiles_per_cta(int block_size, bool prefix) {
     return (block_size == 32 && !prefix) ? PA_PF_QT32 : 2;
 }
 
-template <typename T, int D, int B, bool PREFIX = false>
+template <typename T, int D, int B, bool PREFIX = false, bool WINDOW = false>
 cudaError_t launch_prefill_tc(const pa::PrefillParams& p, const CUtensorMap& k_rows, dim3 grid, cudaStream_t st) {
     constexpr int kQT = prefill_tiles_per_cta(B, PREFIX);
     using Sm = pa::PrefillTcSmem<T, D, B, kQT>;
-    auto kernel = pa::pa_prefill_tc_kernel<T, D, B, PREFIX, kQT>;
+    auto kernel = pa::pa_prefill_tc_kernel<T, D, B, PREFIX, kQT, WINDOW>;
     cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel));
     if (e != cudaSuccess) return e;
     return launch_early(kernel, grid, dim3((6 * kQT + 2) * 32), Sm::kTotal, st, PA_EARLY_LAUNCH, p, k_rows);
@@ -960,11 +964,439 @@ pa_status pa_decode_shared_prefix(void* out, const void* q, const void* key, con
 
 }  // extern "C"
 
-// ---- block management (pa_blocks.cuh)
+// ---- attention with a sliding window, the 4-bit pools, and rotary positions with the cache write
 
 namespace {
 
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// The most blocks of `unit` tokens that hold a visible token of one sequence.
+long long visible_units(long long cap, long long window, long long sinks, int unit) {
+    const long long all = (cap + unit - 1) / unit;
+    if (window <= 0) return all;
+    const long long some = (window + unit - 2) / unit + 1 + (sinks + unit - 1) / unit;
+    return std::min(all, some);
+}
+
+// Partitions of `partition_size` tokens (0: one) that the visible units need.
+long long window_partitions(long long units, int unit, int partition_size) {
+    if (partition_size <= 0) return units > 0 ? 1 : 0;
+    const long long per = partition_size / unit;
+    return (units + per - 1) / per;
+}
+
+// A partition size that gives the device's SMs about `ctas_per_sm` thread
+// blocks each: one pass where the sequences alone do, and no partition of
+// fewer than `least` tokens (a partition's start and merge cost about as much
+// as that many tokens' stream).
+int choose_partition(long long seqs, int num_kv_heads, long long units, int unit, int ctas_per_sm, int least) {
+    const long long pairs = seqs * num_kv_heads;
+    const long long want = static_cast<long long>(ctas_per_sm) * std::max(1, sm_count());
+    if (pairs <= 0 || units <= 0 || pairs >= want) return 0;
+    const long long parts = (want + pairs - 1) / pairs;
+    const long long step = std::max(16, unit);   // partition sizes: multiples of both 16 and the block
+    long long size = (units * unit + parts - 1) / parts;
+    size = std::max<long long>((size + step - 1) / step * step, least);
+    return size >= units * unit || size > INT_MAX / 2 ? 0 : static_cast<int>(size);
+}
+
+pa_status check_window(int window, int num_sinks, int least) {
+    return window < least || num_sinks < 0 ? PA_ERR_INVALID_ARG : PA_OK;
+}
+
+// The partials' place: sets up p for `parts` partitions, or refuses.
+pa_status take_workspace(pa::DecodeParams& p, const DecodeShape& sh, long long parts, void* workspace,
+                         size_t workspace_bytes, int32_t* counters, int64_t num_counters) {
+    p.num_partitions = static_cast<int>(parts);
+    if (parts <= 1) return PA_OK;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < splitk_bytes(sh.num_seqs, sh.num_q_heads, parts, sh.head_dim))
+        return PA_ERR_WORKSPACE;
+    if (!counters || !aligned4(counters) ||
+        num_counters < static_cast<int64_t>(sh.num_seqs) * sh.num_kv_heads)
+        return PA_ERR_WORKSPACE;
+    p.part_acc = static_cast<float*>(workspace);
+    p.part_ml = p.part_acc + static_cast<size_t>(sh.num_seqs) * sh.num_q_heads * parts * sh.head_dim;
+    p.counters = counters;
+    return PA_OK;
+}
+
+template <bool FP8>
+pa_status decode_window(void* out, const void* q, const void* key, const void* value, const void* k_cache,
+                        const void* v_cache, const float* k_scale, const float* v_scale,
+                        const int32_t* block_tables, const int32_t* context_lens, float scale, const DecodeShape& sh,
+                        int window, int num_sinks, int partition_size, void* workspace, size_t workspace_bytes,
+                        int32_t* counters, int64_t num_counters, const int32_t* ref_counts, const int32_t* seq_order,
+                        void* stream) {
+    pa_status st = check_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale, sh);
+    if (st == PA_OK) st = check_scales<FP8>(sh, k_scale, v_scale);
+    if (st == PA_OK) st = check_window(window, num_sinks, 1);
+    if (st != PA_OK) return st;
+    if (partition_size < 0 || partition_size % 16 != 0 || partition_size % sh.block_size != 0)
+        return PA_ERR_INVALID_ARG;
+    if ((key == nullptr) != (value == nullptr) || !aligned16(key) || !aligned16(value)) return PA_ERR_INVALID_ARG;
+    if (!aligned4(seq_order) || !aligned4(ref_counts)) return PA_ERR_INVALID_ARG;
+    if (sh.num_seqs == 0) return PA_OK;
+    pa::DecodeParams p = make_params(out, q, k_cache, v_cache, block_tables, context_lens, scale, sh);
+    p.seq_order = seq_order;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.new_key = key;
+    p.new_value = value;
+    p.ref_counts = ref_counts;
+    p.window = window;
+    p.num_sinks = num_sinks;
+    const long long units = visible_units(p.context_cap, window, num_sinks, sh.block_size);
+    const long long parts = window_partitions(units, sh.block_size, partition_size);
+    if (parts > INT_MAX) return PA_ERR_UNSUPPORTED;
+    st = take_workspace(p, sh, parts, workspace, workspace_bytes, counters, num_counters);
+    if (st != PA_OK) return st;
+    const pa_dtype dtype = static_cast<pa_dtype>(sh.dtype);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (parts > 1) {
+        p.partition_blocks = partition_size / sh.block_size;
+        const dim3 grid(static_cast<unsigned>(parts), sh.num_kv_heads, sh.num_seqs);
+        e = decode_dispatch<true, FP8, false, true>(dtype, sh.head_dim, sh.block_size, p, grid, s);
+    } else {
+        const long long most = std::min<long long>(units * sh.block_size, INT_MAX);
+        const dim3 grid = two_class_grid(p, dim3(1, sh.num_kv_heads, sh.num_seqs), static_cast<int>(most),
+                                         sh.block_size);
+        e = decode_dispatch<false, FP8, false, true>(dtype, sh.head_dim, sh.block_size, p, grid, s);
+    }
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// Calls f(TypeTag<T>, IntTag<D>) for a row kernel's variant; the shape has been validated already.
+template <typename F>
+cudaError_t with_rows(pa_dtype dt, int D, F&& f) {
+    auto by_dim = [&](auto tt) -> cudaError_t { return D == 64 ? f(tt, IntTag<64>{}) : f(tt, IntTag<128>{}); };
+    switch (dt) {
+        case PA_F32: return by_dim(TypeTag<float>{});
+        case PA_F16: return by_dim(TypeTag<__half>{});
+        default: return by_dim(TypeTag<__nv_bfloat16>{});
+    }
+}
+
+pa_status check_row_shape(int64_t num_tokens, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                          int dtype) {
+    if (num_tokens < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype)) return PA_ERR_UNSUPPORTED;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (block_size != 8 && block_size != 16 && block_size != 32) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+template <bool WRITE>
+pa_status rows_int4(void* key, void* value, void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                    int64_t num_tokens, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                    pa_dtype dtype, void* stream) {
+    const pa_status st = check_row_shape(num_tokens, num_kv_heads, head_dim, block_size, num_blocks, dtype);
+    if (st != PA_OK || num_tokens == 0) return st;
+    if (!key || !value || !k_cache || !v_cache || !slot_mapping) return PA_ERR_INVALID_ARG;
+    if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned8(slot_mapping))
+        return PA_ERR_INVALID_ARG;
+    pa::RowsInt4Params p{};
+    p.key = key;
+    p.value = value;
+    p.k_cache = static_cast<uint8_t*>(k_cache);
+    p.v_cache = static_cast<uint8_t*>(v_cache);
+    p.slot_mapping = slot_mapping;
+    p.num_tokens = num_tokens;
+    p.num_kv_heads = num_kv_heads;
+    p.block_size = block_size;
+    p.num_slots = num_blocks * static_cast<long long>(block_size);
+    if (num_tokens > LLONG_MAX / 4096 / num_kv_heads) return PA_ERR_UNSUPPORTED;
+    const long long threads = num_tokens * num_kv_heads * (head_dim * elem_size(dtype) / 16);
+    const long long blocks = (threads + 255) / 256;
+    if (blocks > INT_MAX) return PA_ERR_UNSUPPORTED;
+    const cudaError_t e = with_rows(dtype, head_dim, [&](auto tt, auto dd) -> cudaError_t {
+        using T = typename decltype(tt)::type;
+        constexpr int kD = decltype(dd)::value;
+        return launch_early(WRITE ? pa::pa_reshape_int4_kernel<T, kD> : pa::pa_gather_int4_kernel<T, kD>,
+                            dim3(static_cast<unsigned>(blocks)), dim3(256), 0, static_cast<cudaStream_t>(stream),
+                            PA_EARLY_LAUNCH, p);
+    });
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+template <pa::Pool POOL>
+pa_status rope_and_cache(void* q_out, const void* q, const void* key, const void* value, void* k_cache, void* v_cache,
+                         const float* k_scale, const float* v_scale, const int64_t* positions,
+                         const int64_t* slot_mapping, const float* inv_freq, const void* q_weight,
+                         const void* k_weight, float eps, float rope_scale, int interleaved, int rotary_dim,
+                         int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t num_tokens, int num_q_heads,
+                         int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, pa_dtype dtype,
+                         void* stream) {
+    const pa_status st = check_row_shape(num_tokens, num_kv_heads, head_dim, block_size, num_blocks, dtype);
+    if (st != PA_OK) return st;
+    if (num_q_heads <= 0 || !std::isfinite(eps) || eps < 0.f || !std::isfinite(rope_scale)) return PA_ERR_INVALID_ARG;
+    if (num_q_heads > INT_MAX / 4 || num_kv_heads > INT_MAX / 4) return PA_ERR_UNSUPPORTED;
+    if (rotary_dim < 0 || rotary_dim > head_dim) return PA_ERR_INVALID_ARG;
+    if (rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+    const int per_vec = 16 / elem_size(dtype);
+    if (q_stride < static_cast<int64_t>(num_q_heads) * head_dim ||
+        k_stride < static_cast<int64_t>(num_kv_heads) * head_dim ||
+        v_stride < static_cast<int64_t>(num_kv_heads) * head_dim || q_stride % per_vec || k_stride % per_vec ||
+        v_stride % per_vec)
+        return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (num_tokens > INT_MAX) return PA_ERR_UNSUPPORTED;
+    if (!q_out || !q || !key || !value || !k_cache || !v_cache || !positions || !slot_mapping) return PA_ERR_INVALID_ARG;
+    if (rotary_dim > 0 && !inv_freq) return PA_ERR_INVALID_ARG;
+    if (!aligned16(q_out) || !aligned16(q) || !aligned16(key) || !aligned16(value) || !aligned16(k_cache) ||
+        !aligned16(v_cache) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned8(positions) ||
+        !aligned8(slot_mapping) || !aligned4(inv_freq))
+        return PA_ERR_INVALID_ARG;
+    if (POOL == pa::Pool::kE4m3 && (!k_scale || !v_scale || !aligned4(k_scale) || !aligned4(v_scale)))
+        return PA_ERR_INVALID_ARG;
+    pa::RopeParams p{};
+    p.q_out = q_out;
+    p.q = q;
+    p.key = key;
+    p.value = value;
+    p.k_cache = static_cast<uint8_t*>(k_cache);
+    p.v_cache = static_cast<uint8_t*>(v_cache);
+    p.positions = positions;
+    p.slot_mapping = slot_mapping;
+    p.inv_freq = inv_freq;
+    p.q_weight = q_weight;
+    p.k_weight = k_weight;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.rope_scale = rope_scale;
+    p.eps = eps;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.rotary_dim = rotary_dim;
+    p.block_size = block_size;
+    p.num_slots = num_blocks * static_cast<long long>(block_size);
+    const cudaError_t e = with_rows(dtype, head_dim, [&](auto tt, auto dd) -> cudaError_t {
+        using T = typename decltype(tt)::type;
+        constexpr int kD = decltype(dd)::value;
+        return launch_early(interleaved ? pa::pa_rope_cache_kernel<T, kD, POOL, true>
+                                        : pa::pa_rope_cache_kernel<T, kD, POOL, false>,
+                            dim3(static_cast<unsigned>(num_tokens)), dim3(pa::kRopeThreads), 0,
+                            static_cast<cudaStream_t>(stream), PA_EARLY_LAUNCH, p);
+    });
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// CTAs of the 4-bit decode: warps, and thread blocks an SM holds.
+constexpr int kInt4Warps = 4;
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_rope_and_cache(void* q_out, const void* q, const void* key, const void* value, void* k_cache,
+                            void* v_cache, const int64_t* positions, const int64_t* slot_mapping,
+                            const float* inv_freq, const void* q_weight, const void* k_weight, float eps,
+                            float rope_scale, int interleaved, int rotary_dim, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                            int block_size, int64_t num_blocks, pa_dtype dtype, void* stream) {
+    return rope_and_cache<pa::Pool::kNative>(q_out, q, key, value, k_cache, v_cache, nullptr, nullptr, positions,
+                                             slot_mapping, inv_freq, q_weight, k_weight, eps, rope_scale, interleaved,
+                                             rotary_dim, q_stride, k_stride, v_stride, num_tokens, num_q_heads,
+                                             num_kv_heads, head_dim, block_size, num_blocks, dtype, stream);
+}
+
+pa_status pa_rope_and_cache_fp8(void* q_out, const void* q, const void* key, const void* value, void* k_cache,
+                                void* v_cache, const float* k_scale, const float* v_scale, const int64_t* positions,
+                                const int64_t* slot_mapping, const float* inv_freq, const void* q_weight,
+                                const void* k_weight, float eps, float rope_scale, int interleaved, int rotary_dim,
+                                int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t num_tokens,
+                                int num_q_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                                pa_dtype dtype, void* stream) {
+    return rope_and_cache<pa::Pool::kE4m3>(q_out, q, key, value, k_cache, v_cache, k_scale, v_scale, positions,
+                                           slot_mapping, inv_freq, q_weight, k_weight, eps, rope_scale, interleaved,
+                                           rotary_dim, q_stride, k_stride, v_stride, num_tokens, num_q_heads,
+                                           num_kv_heads, head_dim, block_size, num_blocks, dtype, stream);
+}
+
+pa_status pa_rope_and_cache_int4(void* q_out, const void* q, const void* key, const void* value, void* k_cache,
+                                 void* v_cache, const int64_t* positions, const int64_t* slot_mapping,
+                                 const float* inv_freq, const void* q_weight, const void* k_weight, float eps,
+                                 float rope_scale, int interleaved, int rotary_dim, int64_t q_stride,
+                                 int64_t k_stride, int64_t v_stride, int64_t num_tokens, int num_q_heads,
+                                 int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, pa_dtype dtype,
+                                 void* stream) {
+    return rope_and_cache<pa::Pool::kInt4>(q_out, q, key, value, k_cache, v_cache, nullptr, nullptr, positions,
+                                           slot_mapping, inv_freq, q_weight, k_weight, eps, rope_scale, interleaved,
+                                           rotary_dim, q_stride, k_stride, v_stride, num_tokens, num_q_heads,
+                                           num_kv_heads, head_dim, block_size, num_blocks, dtype, stream);
+}
+
+pa_status pa_reshape_and_cache_int4(const void* key, const void* value, void* k_cache, void* v_cache,
+                                    const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads, int head_dim,
+                                    int block_size, int64_t num_blocks, pa_dtype dtype, void* stream) {
+    return rows_int4<true>(const_cast<void*>(key), const_cast<void*>(value), k_cache, v_cache, slot_mapping,
+                           num_tokens, num_kv_heads, head_dim, block_size, num_blocks, dtype, stream);
+}
+
+pa_status pa_gather_cache_int4(void* key, void* value, const void* k_cache, const void* v_cache,
+                               const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads, int head_dim,
+                               int block_size, int64_t num_blocks, pa_dtype dtype, void* stream) {
+    return rows_int4<false>(key, value, const_cast<void*>(k_cache), const_cast<void*>(v_cache), slot_mapping,
+                            num_tokens, num_kv_heads, head_dim, block_size, num_blocks, dtype, stream);
+}
+
+pa_status pa_decode_int4_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_context_len,
+                              int window, int num_sinks, int* partition_size, size_t* bytes) {
+    if (!partition_size || !bytes || num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+        max_context_len < 0 || *partition_size < -1 || check_window(window, num_sinks, 0) != PA_OK)
+        return PA_ERR_INVALID_ARG;
+    const long long units = visible_units(max_context_len, window, num_sinks, 16);
+    if (*partition_size < 0) *partition_size = choose_partition(num_seqs, num_kv_heads, units, 16, 8, 256);
+    if (*partition_size % 16 != 0) return PA_ERR_INVALID_ARG;
+    const long long parts = window_partitions(units, 16, *partition_size);
+    *bytes = parts > 1 ? splitk_bytes(num_seqs, num_q_heads, parts, head_dim) : 0;
+    return PA_OK;
+}
+
+pa_status pa_decode_int4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                         const int32_t* block_tables, const int32_t* context_lens, float scale, int block_size,
+                         int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_blocks_per_seq,
+                         int max_context_len, int64_t num_blocks, pa_dtype dtype, int window, int num_sinks,
+                         int partition_size, void* workspace, size_t workspace_bytes, int32_t* counters,
+                         int64_t num_counters, const int32_t* seq_order, void* stream) {
+    const DecodeShape sh{block_size, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                         max_context_len, num_blocks, static_cast<int>(dtype)};
+    pa_status st = check_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale, sh);
+    if (st == PA_OK) st = check_window(window, num_sinks, 0);
+    if (st != PA_OK) return st;
+    if (dtype == PA_F32) return PA_ERR_UNSUPPORTED;  // 4-bit pools take 16-bit queries
+    if (partition_size < 0 || partition_size % 16 != 0) return PA_ERR_INVALID_ARG;
+    if (!aligned4(seq_order)) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    pa::DecodeParams p = make_params(out, q, k_cache, v_cache, block_tables, context_lens, scale, sh);
+    p.seq_order = seq_order;
+    p.window = window;
+    p.num_sinks = num_sinks;
+    const long long units = visible_units(p.context_cap, window, num_sinks, 16);
+    const long long parts = window_partitions(units, 16, partition_size);
+    if (parts > INT_MAX) return PA_ERR_UNSUPPORTED;
+    st = take_workspace(p, sh, parts, workspace, workspace_bytes, counters, num_counters);
+    if (st != PA_OK) return st;
+    p.partition_blocks = parts > 1 ? partition_size / 16 : INT_MAX / 2;
+    const dim3 grid(static_cast<unsigned>(std::max(1LL, parts)), num_kv_heads, num_seqs);
+    const cudaError_t e = with_variant(dtype, head_dim, block_size, [&](auto tt, auto dd, auto bb) -> cudaError_t {
+        using T = typename decltype(tt)::type;
+        constexpr int kD = decltype(dd)::value, kB = decltype(bb)::value;
+        if constexpr (pa::IsF32<T>::value) {
+            return cudaErrorInvalidValue;
+        } else {
+            return launch_early(pa::pa_decode_int4_kernel<T, kD, kB, kInt4Warps>, grid, dim3(kInt4Warps * 32), 0,
+                                static_cast<cudaStream_t>(stream), PA_EARLY_LAUNCH, p);
+        }
+    });
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_decode_window_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                int max_context_len, int window, int num_sinks, int* partition_size, size_t* bytes) {
+    if (!partition_size || !bytes || num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+        block_size <= 0 || max_context_len < 0 || *partition_size < -1 ||
+        check_window(window, num_sinks, 1) != PA_OK)
+        return PA_ERR_INVALID_ARG;
+    const long long units = visible_units(max_context_len, window, num_sinks, block_size);
+    if (*partition_size < 0)
+        *partition_size = choose_partition(num_seqs, num_kv_heads, units, block_size, 4, 256);
+    if (*partition_size % 16 != 0 || *partition_size % block_size != 0) return PA_ERR_INVALID_ARG;
+    const long long parts = window_partitions(units, block_size, *partition_size);
+    *bytes = parts > 1 ? splitk_bytes(num_seqs, num_q_heads, parts, head_dim) : 0;
+    return PA_OK;
+}
+
+pa_status pa_decode_window(void* out, const void* q, const void* key, const void* value, void* k_cache, void* v_cache,
+                           const int32_t* block_tables, const int32_t* context_lens, float scale, int block_size,
+                           int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_blocks_per_seq,
+                           int max_context_len, int64_t num_blocks, pa_dtype dtype, int window, int num_sinks,
+                           int partition_size, void* workspace, size_t workspace_bytes, int32_t* counters,
+                           int64_t num_counters, const int32_t* ref_counts, const int32_t* seq_order, void* stream) {
+    const DecodeShape sh{block_size, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                         max_context_len, num_blocks, static_cast<int>(dtype)};
+    return decode_window<false>(out, q, key, value, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens,
+                                scale, sh, window, num_sinks, partition_size, workspace, workspace_bytes, counters,
+                                num_counters, ref_counts, seq_order, stream);
+}
+
+pa_status pa_decode_window_fp8(void* out, const void* q, const void* key, const void* value, void* k_cache,
+                               void* v_cache, const float* k_scale, const float* v_scale,
+                               const int32_t* block_tables, const int32_t* context_lens, float scale, int block_size,
+                               int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_blocks_per_seq,
+                               int max_context_len, int64_t num_blocks, pa_dtype dtype, int window, int num_sinks,
+                               int partition_size, void* workspace, size_t workspace_bytes, int32_t* counters,
+                               int64_t num_counters, const int32_t* ref_counts, const int32_t* seq_order,
+                               void* stream) {
+    const DecodeShape sh{block_size, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                         max_context_len, num_blocks, static_cast<int>(dtype)};
+    return decode_window<true>(out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                               scale, sh, window, num_sinks, partition_size, workspace, workspace_bytes, counters,
+                               num_counters, ref_counts, seq_order, stream);
+}
+
+pa_status pa_prefill_window(void* out, const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_tables, const int32_t* context_lens, const int32_t* query_start,
+                            float scale, int block_size, int num_seqs, int num_q_heads, int num_kv_heads,
+                            int head_dim, int max_blocks_per_seq, int max_context_len, int max_query_len,
+                            int64_t num_blocks, pa_dtype dtype, int window, int num_sinks, void* stream) {
+    const DecodeShape sh{block_size, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                         max_context_len, num_blocks, static_cast<int>(dtype)};
+    pa_status st = check_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale, sh);
+    if (st == PA_OK) st = check_window(window, num_sinks, 1);
+    if (st != PA_OK) return st;
+    if (dtype == PA_F32) return PA_ERR_UNSUPPORTED;  // the tensor-core path takes 16-bit inputs
+    if (scale <= 0.f || max_query_len < 0) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || max_query_len == 0) return PA_OK;
+    if (!query_start || !aligned4(query_start)) return PA_ERR_INVALID_ARG;
+    CUtensorMap k_rows{};
+    if (!prefill_k_source(&k_rows, k_cache, dtype, block_size, head_dim, num_kv_heads, num_blocks))
+        return PA_ERR_UNSUPPORTED;
+    pa::PrefillParams p{};
+    p.out = out;
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.query_start = query_start;
+    p.score_scale = scale * 1.4426950408889634f;
+    p.num_seqs = num_seqs;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = num_q_heads / num_kv_heads;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.context_cap = context_cap(sh);
+    p.num_blocks = num_blocks;
+    p.tile_tokens = 128 / p.group;
+    p.window = window;
+    p.num_sinks = num_sinks;
+    const long long per_cta = static_cast<long long>(prefill_tiles_per_cta(block_size, false)) * p.tile_tokens;
+    const long long tiles = (static_cast<long long>(max_query_len) + per_cta - 1) / per_cta;
+    if (tiles > INT_MAX) return PA_ERR_UNSUPPORTED;
+    const dim3 grid(static_cast<unsigned>(tiles), num_kv_heads, num_seqs);
+    const cudaError_t e = with_variant(dtype, head_dim, block_size, [&](auto tt, auto dd, auto bb) -> cudaError_t {
+        using T = typename decltype(tt)::type;
+        constexpr int kD = decltype(dd)::value, kB = decltype(bb)::value;
+        if constexpr (pa::IsF32<T>::value) {
+            return cudaErrorInvalidValue;
+        } else {
+            return launch_prefill_tc<T, kD, kB, false, true>(p, k_rows, grid, static_cast<cudaStream_t>(stream));
+        }
+    });
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// ---- block management (pa_blocks.cuh)
+
+namespace {
 
 pa_status check_block_state(const int32_t* ref_counts, const int32_t* free_ids, const int64_t* free_state,
                             int64_t num_blocks) {

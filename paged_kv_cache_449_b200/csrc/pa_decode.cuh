@@ -71,6 +71,11 @@ struct DecodeParams {
     // partitions fill the slots before it); the last of the num_partitions
     // arrivals on counters[s * Hkv + kvh] merges them
     int first_block;
+    // sliding window (0: none): the newest `window` tokens and the first
+    // num_sinks ones are attended; the logical blocks that hold none of them
+    // are left out, and a partition counts the blocks that are taken
+    int window;
+    int num_sinks;
 };
 
 // Append: the newest token of sequence s (logical position L-1) is written
@@ -222,7 +227,7 @@ struct DecodeSmem {
 #define PA_PREFIX_MIN_CTAS 5
 #endif
 template <typename T, int D, int B, int NW, int STAGES, bool SPLIT, bool FP8 = false, bool CLASSES = false,
-          bool PREFIX = false>
+          bool PREFIX = false, bool WINDOW = false>
 __global__ void __launch_bounds__(NW * 32, (PREFIX && NW <= 4) ? PA_PREFIX_MIN_CTAS : 1)
     pa_decode_kernel(const __grid_constant__ DecodeParams p) {
     using Smem = DecodeSmem<T, D, B, NW, STAGES, FP8>;
@@ -233,6 +238,7 @@ __global__ void __launch_bounds__(NW * 32, (PREFIX && NW <= 4) ? PA_PREFIX_MIN_C
     constexpr int kTile = Smem::kTile;
     static_assert(STAGES >= 1 && STAGES <= 32, "ring depth");
     static_assert(!(PREFIX && (SPLIT || FP8 || kF32)), "the shared-prefix form is one pass over 16-bit pools");
+    static_assert(!(PREFIX && WINDOW), "the shared-prefix form attends the whole context");
     static_assert((kTile % 16) == 0, "bulk copies move multiples of 16 bytes");
 
     extern __shared__ __align__(128) uint8_t smem[];
@@ -285,7 +291,9 @@ __global__ void __launch_bounds__(NW * 32, (PREFIX && NW <= 4) ? PA_PREFIX_MIN_C
     const int b0_first = SPLIT ? part * p.partition_blocks : (PREFIX ? p.first_block : 0);
     const int32_t* bt = p.block_tables + static_cast<long long>(s) * p.max_blocks_per_seq + b0_first + warp;
     int first_ids = -1;
-    if (b0_first + warp + lane * NW < p.max_blocks_per_seq) first_ids = __ldg(bt + lane * NW);
+    if constexpr (!WINDOW) {   // (with a window, which blocks come first depends on the context length)
+        if (b0_first + warp + lane * NW < p.max_blocks_per_seq) first_ids = __ldg(bt + lane * NW);
+    }
     const T* qrows = reinterpret_cast<const T*>(p.q) +
                      (static_cast<long long>(s) * p.num_q_heads + kvh * group) * D;
     typename WarpState<TM, D, B>::type acc;
@@ -304,15 +312,49 @@ __global__ void __launch_bounds__(NW * 32, (PREFIX && NW <= 4) ? PA_PREFIX_MIN_C
         if (threadIdx.x == 0 && part == 0 && kvh == 0) flag_error(2 /* PA_DEVERR_CONTEXT_LEN */);
         L = L < 0 ? 0 : p.context_cap;
     }
+    // The sliding window's blocks: `taken` of them, logical block logical(i) =
+    // i up to the last one of the first num_sinks tokens, then those from the
+    // window's first on.
+    int wlo = 0, sinks = 0, taken = (L + B - 1) / B, sink_blocks = taken, gap = 0;
+    if constexpr (WINDOW) {
+        wlo = L > p.window ? L - p.window : 0;
+        sinks = min(p.num_sinks, L);
+        const int sb = (sinks + B - 1) / B;
+        if (wlo / B > sb) {
+            sink_blocks = sb;
+            gap = wlo / B - sb;
+            taken -= gap;
+        }
+    }
+    auto logical = [&](int i) -> int {
+        if constexpr (WINDOW) return i < sink_blocks ? i : i + gap;
+        return i;
+    };
+    // the attended tokens of logical block j (id: its block id, negative if refused)
+    auto attended = [&](int id, int j) {
+        const int valid = id < 0 ? 0 : min(B, L - j * B);
+        if constexpr (WINDOW) {
+            uint32_t bits = valid >= 32 ? 0xffffffffu : (1u << max(valid, 0)) - 1u;
+            const int lo = wlo - j * B, sk = sinks - j * B;   // left out: tokens sk <= t < lo of the block
+            if (lo > 0 && lo > sk) {
+                const uint32_t below = lo >= 32 ? 0xffffffffu : (1u << lo) - 1u;
+                const uint32_t first = sk <= 0 ? 0u : (sk >= 32 ? 0xffffffffu : (1u << sk) - 1u);
+                bits &= ~below | first;
+            }
+            return TokenBits{bits};
+        } else {
+            return valid;
+        }
+    };
     // Two classes (no copy is in flight yet): this half of the grid leaves the
     // sequence to the other half.
     if constexpr (CLASSES) {
-        if (p.class_threshold > 0 && (L >= p.class_threshold) != (blockIdx.z < static_cast<unsigned>(p.num_seqs))) {
+        if (p.class_threshold > 0 && ((WINDOW ? taken * B : L) >= p.class_threshold) != (blockIdx.z < static_cast<unsigned>(p.num_seqs))) {
             prefix_pass_done();
             return;
         }
     }
-    const int nblk = (L + B - 1) / B;
+    const int nblk = taken;   // blocks attended
     int b0 = 0, b1 = nblk;
     if constexpr (SPLIT) {
         b0 = part * p.partition_blocks;
@@ -368,7 +410,10 @@ __global__ void __launch_bounds__(NW * 32, (PREFIX && NW <= 4) ? PA_PREFIX_MIN_C
         const int i = round * 32 + lane;
         int id = -1;
         if (i < n_w) {
-            id = round == 0 ? first_ids : __ldg(bt + i * NW);
+            if constexpr (WINDOW)
+                id = __ldg(p.block_tables + static_cast<long long>(s) * p.max_blocks_per_seq + logical(b0 + warp + i * NW));
+            else
+                id = round == 0 ? first_ids : __ldg(bt + i * NW);
             if (id < 0 || static_cast<long long>(id) >= p.num_blocks) {
                 flag_error(1 /* PA_DEVERR_BLOCK_ID */);
                 id = -1;
@@ -414,7 +459,7 @@ __global__ void __launch_bounds__(NW * 32, (PREFIX && NW <= 4) ? PA_PREFIX_MIN_C
     if (owns_last && p.ref_counts != nullptr) {
         // Copy-on-write guard: the block the newest token goes to must be held
         // by this sequence alone.  Checked while the first copies are in flight.
-        const int id = __ldg(p.block_tables + static_cast<long long>(s) * p.max_blocks_per_seq + last_block);
+        const int id = __ldg(p.block_tables + static_cast<long long>(s) * p.max_blocks_per_seq + logical(last_block));
         if (id >= 0 && id < p.num_blocks && __ldg(p.ref_counts + id) != 1) {
             if (lane == 0) flag_error(128 /* PA_DEVERR_SHARED_BLOCK */);
             owns_last = false;  // no write; the pool is attended as it is
@@ -456,8 +501,7 @@ __global__ void __launch_bounds__(NW * 32, (PREFIX && NW <= 4) ? PA_PREFIX_MIN_C
                 }
                 const int id0 = block_id(i), id1 = block_id(i + 1);
                 const int j0 = b0 + warp + i * NW, j1 = j0 + NW;
-                const int valid0 = id0 < 0 ? 0 : min(B, L - j0 * B);
-                const int valid1 = id1 < 0 ? 0 : min(B, L - j1 * B);
+                const auto valid0 = attended(id0, logical(j0)), valid1 = attended(id1, logical(j1));
                 uint8_t* stage0 = wring + st0 * 2 * kTile;
                 uint8_t* stage1 = wring + st1 * 2 * kTile;
                 if (owns_last) {
@@ -494,8 +538,8 @@ __global__ void __launch_bounds__(NW * 32, (PREFIX && NW <= 4) ? PA_PREFIX_MIN_C
             break;
         }
         const int id = block_id(i);
-        const int j = b0 + warp + i * NW;  // logical block index
-        const int valid = id < 0 ? 0 : min(B, L - j * B);
+        const int j = b0 + warp + i * NW;  // logical block index (with a window: of those taken)
+        const auto valid = attended(id, logical(j));
         uint8_t* stage = wring + st * 2 * kTile;
         if constexpr (FP8) {
             if (owns_last && j == last_block && id >= 0)

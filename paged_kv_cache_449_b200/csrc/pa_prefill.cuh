@@ -62,6 +62,10 @@ struct PrefillParams {
     int prefix_len;
     int prefix_tiles;
     int prefix_append;
+    // sliding window (the tensor-core kernel's WINDOW form): the query at
+    // position p attends to keys t <= p with t > p - window or t < num_sinks
+    int window;
+    int num_sinks;
 };
 
 template <typename T, int D, int B, int NW, int STAGES>

@@ -241,7 +241,7 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile
 // Warps 0-3 and 4-7: softmax of query tile 0 and 1 (thread = row = tensor-memory
 // lane); warps 8 / 9 issue S = Q K^T and 10 / 11 O += P V for query tile 0 / 1;
 // warps 12 and 13 fetch K and V (QT = 1: warps 0-3, 4, 5, 6 and 7).
-template <typename T, int D, int B, bool PREFIX = false, int QT = 2>
+template <typename T, int D, int B, bool PREFIX = false, int QT = 2, bool WINDOW = false>
 __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill_tc_kernel(const __grid_constant__ PrefillParams p,
                                                                 const __grid_constant__ CUtensorMap k_rows) {
     using Sm = PrefillTcSmem<T, D, B, QT>;
@@ -258,6 +258,7 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
     static_assert(kPCol + kKeys <= 256, "tensor memory budget");
     static_assert(B == 8 || B == 16 || B == 32, "8-, 16- or 32-token blocks");
     static_assert(D == 64 || D == 128, "head dims");
+    static_assert(!(PREFIX && WINDOW), "a shared prefix is attended whole");
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sm::kBarOff);
     uint64_t* k_full = bars;         // [KS] K tiles of a key tile landed
@@ -318,6 +319,29 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
             nt[q] = tok0[q] < Q ? ((L - Q + tok1[q] - 1) / B + kBlocks) / kBlocks : 0;
         }
     }
+    // Sliding window: wlo is the first key that the window of the CTA's first
+    // query reaches.  The key tiles taken are those of the sinks and those from
+    // wlo's on (nt counts them; `gap` tiles in between are left out); a block
+    // without a visible key is not fetched, whatever its table entry holds.
+    int wlo = 0, sink_tiles = INT_MAX, gap = 0;
+    if constexpr (WINDOW) {
+        wlo = max(0, L - Q + tok0[0] - p.window + 1);
+        const int st = (min(p.num_sinks, L) + kKeys - 1) / kKeys;
+        if (wlo / kKeys > st) {
+            sink_tiles = st;
+            gap = wlo / kKeys - st;
+        }
+        nt[0] -= nt[0] > 0 ? gap : 0;
+        nt[1] -= nt[1] > 0 ? gap : 0;
+    }
+    auto key_tile = [&](int j) -> int {   // the j-th key tile of this CTA
+        if constexpr (WINDOW) return j < sink_tiles ? j : j + gap;
+        return tb + j;
+    };
+    auto block_seen = [&](int jb) -> bool {   // whether any query of the CTA sees a key of block jb
+        if constexpr (WINDOW) return jb * B + B > wlo || jb * B < p.num_sinks;
+        return true;
+    };
     // Shared-prefix form, the CTA's last step: its sequences [tok0[0], seq_end)
     // arrive on their (sequence, kv head) counters once its partials are
     // written (`empty`: empty partials written here first); the last of the
@@ -420,15 +444,15 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
     auto load_ids = [&](int j, int (&ids)[kBlocks]) {
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
-            const int jb = (tb + j) * kBlocks + b;
-            ids[b] = (j < ntiles && jb < nblk) ? __ldg(table + jb) : -1;
+            const int jb = key_tile(j) * kBlocks + b;
+            ids[b] = (j < ntiles && jb < nblk && block_seen(jb)) ? __ldg(table + jb) : -1;
         }
     };
     // The same mask computed by a whole warp: lane b loads block b's id (the
     // id of lane `lane` for tile j; -1 past the need), a ballot gathers them.
     auto lane_id = [&](int j) -> int {
-        const int jb = (tb + j) * kBlocks + lane;
-        return (lane < kBlocks && j < ntiles && jb < nblk) ? __ldg(table + jb) : -1;
+        const int jb = key_tile(j) * kBlocks + lane;
+        return (lane < kBlocks && j < ntiles && jb < nblk && block_seen(jb)) ? __ldg(table + jb) : -1;
     };
     auto ok_ballot = [&](int id) -> uint32_t {
         return __ballot_sync(0xffffffffu, id >= 0 && static_cast<long long>(id) < p.num_blocks);
@@ -458,7 +482,8 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
         if (!v_side) {
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
-                if ((tb + j) * kBlocks + b < nblk && !((ok >> b) & 1u)) flag_error(1 /* PA_DEVERR_BLOCK_ID */);
+                if (const int jb = key_tile(j) * kBlocks + b; jb < nblk && block_seen(jb) && !((ok >> b) & 1u))
+                    flag_error(1 /* PA_DEVERR_BLOCK_ID */);
             if constexpr (B == 8) {
                 // 8-token blocks: a (block, head) tile, [D/8][8][8], is already a
                 // column of core matrices of the S MMA's K-major operand, so the
@@ -637,12 +662,41 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
             const int vst = j % VS;
             if (!__all_sync(0xffffffffu, tc_wait(&v_full[vst], (j / VS) & 1, abort))) break;
             if constexpr (!PREFIX) {   // (a shared prefix ends on a block boundary: no tail)
-                const int lb = (L - 1) / B - j * kBlocks;
+                const int lb = (L - 1) / B - key_tile(j) * kBlocks;
                 if (lb >= 0 && lb < kBlocks && ((ok >> lb) & 1u)) {
                     uint8_t* vt = smem + Sm::kVOff + vst * Sm::kStage + lb * kTile;
                     const int t_from = (L - 1) % B + 1;
                     for (int i = lane; i < (B - t_from) * (D / 8); i += 32) {
                         const int t = t_from + i / (D / 8), c = i % (D / 8);
+                        *reinterpret_cast<uint4*>(vt + (c * B + t) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+            }
+            if constexpr (B == 8) {
+                // a block fetched in another's place (see the V producer): its
+                // keys have P = 0, so its rows are zeroed too
+                uint32_t stand_in = (((ok & 0x55u) << 1) | ((ok & 0xaau) >> 1)) & ~ok;
+                if (stand_in != 0u) {
+                    for (; stand_in != 0u; stand_in &= stand_in - 1u) {
+                        uint8_t* vt = smem + Sm::kVOff + vst * Sm::kStage + (__ffs(stand_in) - 1) * kTile;
+                        for (int i = lane; i < kTile / 16; i += 32)
+                            *reinterpret_cast<uint4*>(vt + i * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+            }
+            if constexpr (WINDOW) {
+                // rows before the window that no query of the CTA sees: the same
+                for (int b = 0; b < kBlocks; ++b) {
+                    const int first = (key_tile(j) * kBlocks + b) * B;
+                    const int from = max(0, p.num_sinks - first), to = min(B, wlo - first);
+                    if (from >= to || !((ok >> b) & 1u)) continue;
+                    uint8_t* vt = smem + Sm::kVOff + vst * Sm::kStage + b * kTile;
+                    for (int i = lane; i < (to - from) * (D / 8); i += 32) {
+                        const int t = from + i / (D / 8), c = i % (D / 8);
                         *reinterpret_cast<uint4*>(vt + (c * B + t) * 16) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
@@ -710,10 +764,12 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
             tc::fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(sfree);
-            const int key0 = (tb + j) * kKeys;
+            const int key0 = key_tile(j) * kKeys;
             // row maximum over eight independent partial maxima (no 64-long chain)
             float m8[8];
-            if (ok == all_blocks && key0 + kKeys - 1 <= row_pos) {
+            bool all_seen = ok == all_blocks && key0 + kKeys - 1 <= row_pos;
+            if constexpr (WINDOW) all_seen = all_seen && (key0 > row_pos - p.window || key0 + kKeys <= p.num_sinks);
+            if (all_seen) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) m8[c] = sv[c];
 #pragma unroll
@@ -721,7 +777,8 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
             } else {
 #pragma unroll
                 for (int c = 0; c < kKeys; ++c) {
-                    const bool vis = ((ok >> (c / B)) & 1u) && key0 + c <= row_pos;
+                    bool vis = ((ok >> (c / B)) & 1u) && key0 + c <= row_pos;
+                    if constexpr (WINDOW) vis = vis && (key0 + c > row_pos - p.window || key0 + c < p.num_sinks);
                     sv[c] = vis ? sv[c] : kNegInf;
                     m8[c & 7] = c < 8 ? sv[c] : fmaxf(m8[c & 7], sv[c]);
                 }

@@ -46,6 +46,19 @@ struct IsF32<float> {
 // (8x8 transpose) per 8 tokens.  The query heads of a GQA group fill the N
 // dimension (g <= 8), so no MMA row is padding.
 
+// The tokens of a staged block that are attended: the first `valid` ones (an
+// int), or, with a sliding window, any set of them (TokenBits).
+struct TokenBits {
+    uint32_t bits;
+};
+__device__ __forceinline__ bool token_in(int t, int valid) { return t < valid; }
+__device__ __forceinline__ bool token_in(int t, TokenBits m) { return (m.bits >> t) & 1u; }
+// Whether some of the 16 tokens from 16 tg on are left out.
+__device__ __forceinline__ bool tokens_partial(int tg, int valid) { return valid < tg * 16 + 16; }
+__device__ __forceinline__ bool tokens_partial(int tg, TokenBits m) {
+    return ((m.bits >> (16 * tg)) & 0xffffu) != 0xffffu;
+}
+
 template <typename T, int D, int B>
 struct WarpMma {
     static constexpr int kMt = D / 16;  // 16-row tiles of head_dim in O^T
@@ -78,17 +91,18 @@ struct WarpMma {
     __device__ __forceinline__ void load_q(const T* q_rows, int group, int lane) { fetch_q(qa, q_rows, group, lane); }
 
     // Zero the 16-bit halves of a V fragment register that belong to tokens
-    // >= valid (token `tok` in the low half, tok+1 in the high half).
-    static __device__ __forceinline__ uint32_t mask_pair(uint32_t v, int tok, int valid) {
-        const uint32_t keep = (tok < valid ? 0x0000ffffu : 0u) | (tok + 1 < valid ? 0xffff0000u : 0u);
+    // that are not attended (token `tok` in the low half, tok+1 in the high half).
+    template <typename V>
+    static __device__ __forceinline__ uint32_t mask_pair(uint32_t v, int tok, V valid) {
+        const uint32_t keep = (token_in(tok, valid) ? 0x0000ffffu : 0u) | (token_in(tok + 1, valid) ? 0xffff0000u : 0u);
         return v & keep;
     }
 
     // One block of B tokens: K tile at kbase, V tile at vbase (shared memory,
     // layout [D/8][B][8]; E4M3: the 8-bit pools' K and V tile layouts, codes
     // widened to fp16 in registers); tokens >= valid are masked out.
-    template <bool E4M3 = false>
-    __device__ __forceinline__ void block(uint32_t kbase, uint32_t vbase, int valid, int group, float scale_log2,
+    template <bool E4M3 = false, typename V = int>
+    __device__ __forceinline__ void block(uint32_t kbase, uint32_t vbase, V valid, int group, float scale_log2,
                                           int lane) {
         const int r = lane >> 2, c = lane & 3;
         const int mtx = lane >> 3, row = lane & 7;
@@ -132,10 +146,10 @@ struct WarpMma {
 
             // Online softmax per head (column) over the 16 tokens (rows).
             const int t_lo = tg * 16 + r, t_hi = t_lo + 8;
-            float x0 = (h0ok && t_lo < valid) ? sc[0] * scale_log2 : kNegInf;
-            float x1 = (h1ok && t_lo < valid) ? sc[1] * scale_log2 : kNegInf;
-            float x2 = (h0ok && t_hi < valid) ? sc[2] * scale_log2 : kNegInf;
-            float x3 = (h1ok && t_hi < valid) ? sc[3] * scale_log2 : kNegInf;
+            float x0 = (h0ok && token_in(t_lo, valid)) ? sc[0] * scale_log2 : kNegInf;
+            float x1 = (h1ok && token_in(t_lo, valid)) ? sc[1] * scale_log2 : kNegInf;
+            float x2 = (h0ok && token_in(t_hi, valid)) ? sc[2] * scale_log2 : kNegInf;
+            float x3 = (h1ok && token_in(t_hi, valid)) ? sc[3] * scale_log2 : kNegInf;
             float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
@@ -162,7 +176,7 @@ struct WarpMma {
             // P^T from the accumulator layout to the B operand of O^T += V^T P^T.
             const uint32_t b0 = movmatrix_trans(Mma<T>::pack(p0, p1));  // tokens 0..7 of the group
             const uint32_t b1 = movmatrix_trans(Mma<T>::pack(p2, p3));  // tokens 8..15
-            const bool partial = valid < tg * 16 + 16;
+            const bool partial = tokens_partial(tg, valid);
             if constexpr (B >= 16) {
                 const int tlo = tg * 16 + 2 * c, thi = tlo + 8;
 #pragma unroll
@@ -218,20 +232,21 @@ struct WarpMma {
     // maximum, one rescale of O^T and the running sums for the 32 tokens.
     // Scores S^T of block a in sa, of block b in sb; returns the P^T operands
     // of both blocks.
-    __device__ __forceinline__ void softmax_step2(const float (&sa)[4], const float (&sb)[4], int valid_a,
-                                                  int valid_b, int group, float scale_log2, int lane,
+    template <typename V>
+    __device__ __forceinline__ void softmax_step2(const float (&sa)[4], const float (&sb)[4], V valid_a,
+                                                  V valid_b, int group, float scale_log2, int lane,
                                                   uint32_t (&pa)[2], uint32_t (&pb)[2]) {
         const int r = lane >> 2, c = lane & 3;
         const bool h0ok = 2 * c < group, h1ok = 2 * c + 1 < group;
         const int t_lo = r, t_hi = r + 8;
-        const float xa0 = (h0ok && t_lo < valid_a) ? sa[0] * scale_log2 : kNegInf;
-        const float xa1 = (h1ok && t_lo < valid_a) ? sa[1] * scale_log2 : kNegInf;
-        const float xa2 = (h0ok && t_hi < valid_a) ? sa[2] * scale_log2 : kNegInf;
-        const float xa3 = (h1ok && t_hi < valid_a) ? sa[3] * scale_log2 : kNegInf;
-        const float xb0 = (h0ok && t_lo < valid_b) ? sb[0] * scale_log2 : kNegInf;
-        const float xb1 = (h1ok && t_lo < valid_b) ? sb[1] * scale_log2 : kNegInf;
-        const float xb2 = (h0ok && t_hi < valid_b) ? sb[2] * scale_log2 : kNegInf;
-        const float xb3 = (h1ok && t_hi < valid_b) ? sb[3] * scale_log2 : kNegInf;
+        const float xa0 = (h0ok && token_in(t_lo, valid_a)) ? sa[0] * scale_log2 : kNegInf;
+        const float xa1 = (h1ok && token_in(t_lo, valid_a)) ? sa[1] * scale_log2 : kNegInf;
+        const float xa2 = (h0ok && token_in(t_hi, valid_a)) ? sa[2] * scale_log2 : kNegInf;
+        const float xa3 = (h1ok && token_in(t_hi, valid_a)) ? sa[3] * scale_log2 : kNegInf;
+        const float xb0 = (h0ok && token_in(t_lo, valid_b)) ? sb[0] * scale_log2 : kNegInf;
+        const float xb1 = (h1ok && token_in(t_lo, valid_b)) ? sb[1] * scale_log2 : kNegInf;
+        const float xb2 = (h0ok && token_in(t_hi, valid_b)) ? sb[2] * scale_log2 : kNegInf;
+        const float xb3 = (h1ok && token_in(t_hi, valid_b)) ? sb[3] * scale_log2 : kNegInf;
         float mx0 = fmaxf(fmaxf(xa0, xa2), fmaxf(xb0, xb2));
         float mx1 = fmaxf(fmaxf(xa1, xa3), fmaxf(xb1, xb3));
 #pragma unroll
@@ -298,9 +313,9 @@ struct WarpMma {
 
     // Two blocks of 16 tokens (a, b) in one step: the K and V tiles of each
     // staged as block() takes them; tokens >= valid_a (valid_b) masked out.
-    template <bool E4M3 = false>
-    __device__ __forceinline__ void block2(uint32_t ka, uint32_t va, int valid_a, uint32_t kb, uint32_t vb,
-                                           int valid_b, int group, float scale_log2, int lane) {
+    template <bool E4M3 = false, typename V = int>
+    __device__ __forceinline__ void block2(uint32_t ka, uint32_t va, V valid_a, uint32_t kb, uint32_t vb,
+                                           V valid_b, int group, float scale_log2, int lane) {
         static_assert(B == 16, "16-token blocks");
         const int c = lane & 3;
         float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
@@ -320,13 +335,13 @@ struct WarpMma {
             uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
             v_frag<E4M3>(va, mt, lane, a0, a1, a2, a3);
             v_frag<E4M3>(vb, mt, lane, b0, b1, b2, b3);
-            if (valid_a < 16) {
+            if (tokens_partial(0, valid_a)) {
                 a0 = mask_pair(a0, tlo, valid_a);
                 a1 = mask_pair(a1, tlo, valid_a);
                 a2 = mask_pair(a2, thi, valid_a);
                 a3 = mask_pair(a3, thi, valid_a);
             }
-            if (valid_b < 16) {
+            if (tokens_partial(0, valid_b)) {
                 b0 = mask_pair(b0, tlo, valid_b);
                 b1 = mask_pair(b1, tlo, valid_b);
                 b2 = mask_pair(b2, thi, valid_b);
@@ -441,7 +456,8 @@ struct WarpF32 {
         qs = slot;
     }
 
-    __device__ __forceinline__ void block(const float* ktile, const float* vtile, int valid, int group, float scale,
+    template <typename V>
+    __device__ __forceinline__ void block(const float* ktile, const float* vtile, V valid, int group, float scale,
                                           int lane) {
         const int t = lane % B, part = lane / B;
         float s[kMaxGroup];
@@ -471,7 +487,7 @@ struct WarpF32 {
             }
 #pragma unroll
             for (int off = B; off < 32; off <<= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], off);
-            const float x = (t < valid) ? s[h] * scale : kNegInf;
+            const float x = token_in(t, valid) ? s[h] * scale : kNegInf;
             float mx = x;
 #pragma unroll
             for (int off = 1; off < B; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
@@ -497,7 +513,7 @@ struct WarpF32 {
         for (int ii = 0; ii < kPer; ++ii) {
             const int tt = ((ii + cj) % kPer) * kGrp + tg;  // rotated so a quarter-warp hits 8 banks
             float4 vv = *reinterpret_cast<const float4*>(vtile + (cj * B + tt) * 4);
-            if (tt >= valid) vv = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!token_in(tt, valid)) vv = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int h = 0; h < kMaxGroup; ++h) {
                 const float ph = __shfl_sync(0xffffffffu, p[h], tt);
