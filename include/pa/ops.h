@@ -117,10 +117,10 @@ pa_status pa_gather_cache_int4(void* key, void* value, const void* k_cache, cons
  * The decode entries below share a plan:
  *   partition_size  0: one thread block per (sequence, kv head); otherwise the
  *                   visible tokens are split into partitions of this many
- *                   (counted in whole blocks; 4-bit pools: in units of 16
+ *                   (counted in whole blocks; 4-bit pools: in steps of 32
  *                   tokens) and the last thread block of a (sequence, kv head)
  *                   to finish merges them, as pa_decode_splitk does with
- *                   counters.  A multiple of 16 and of block_size (4-bit: of 16).
+ *                   counters.  A multiple of 16 and of block_size (4-bit: of 32).
  *   workspace,
  *   counters        as in pa_decode_splitk with counters; not read where one
  *                   partition holds every visible token (NULL is fine there)

@@ -143,8 +143,8 @@ def load_library(path: str) -> ctypes.CDLL:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:   # (the raw handle: making a Stream object costs 3 us, as much as a launch)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

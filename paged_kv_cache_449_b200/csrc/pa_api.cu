@@ -1186,8 +1186,17 @@ pa_status rope_and_cache(void* q_out, const void* q, const void* key, const void
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// CTAs of the 4-bit decode: warps, and thread blocks an SM holds.
-constexpr int kInt4Warps = 4;
+// CTAs of the 4-bit decode: 4 warps, four CTAs per SM, each warp with a ring
+// of 32-token stages (13.8 KB; 9/8 bytes an element of K and V).
+#ifndef PA_INT4_WARPS
+#define PA_INT4_WARPS 4
+#endif
+#ifndef PA_INT4_RING
+#define PA_INT4_RING 13824
+#endif
+constexpr int kInt4Step = 32;
+template <int D>
+constexpr int kInt4Stages = PA_INT4_RING / (2 * pa::int4_tile_bytes(kInt4Step, D));
 
 }  // namespace
 
@@ -1250,10 +1259,10 @@ pa_status pa_decode_int4_plan(int num_seqs, int num_q_heads, int num_kv_heads, i
     if (!partition_size || !bytes || num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
         max_context_len < 0 || *partition_size < -1 || check_window(window, num_sinks, 0) != PA_OK)
         return PA_ERR_INVALID_ARG;
-    const long long units = visible_units(max_context_len, window, num_sinks, 16);
-    if (*partition_size < 0) *partition_size = choose_partition(num_seqs, num_kv_heads, units, 16, 8, 256);
-    if (*partition_size % 16 != 0) return PA_ERR_INVALID_ARG;
-    const long long parts = window_partitions(units, 16, *partition_size);
+    const long long units = visible_units(max_context_len, window, num_sinks, kInt4Step);
+    if (*partition_size < 0) *partition_size = choose_partition(num_seqs, num_kv_heads, units, kInt4Step, 8, 256);
+    if (*partition_size % kInt4Step != 0) return PA_ERR_INVALID_ARG;
+    const long long parts = window_partitions(units, kInt4Step, *partition_size);
     *bytes = parts > 1 ? splitk_bytes(num_seqs, num_q_heads, parts, head_dim) : 0;
     return PA_OK;
 }
@@ -1270,19 +1279,19 @@ pa_status pa_decode_int4(void* out, const void* q, const void* k_cache, const vo
     if (st == PA_OK) st = check_window(window, num_sinks, 0);
     if (st != PA_OK) return st;
     if (dtype == PA_F32) return PA_ERR_UNSUPPORTED;  // 4-bit pools take 16-bit queries
-    if (partition_size < 0 || partition_size % 16 != 0) return PA_ERR_INVALID_ARG;
+    if (partition_size < 0 || partition_size % kInt4Step != 0) return PA_ERR_INVALID_ARG;
     if (!aligned4(seq_order)) return PA_ERR_INVALID_ARG;
     if (num_seqs == 0) return PA_OK;
     pa::DecodeParams p = make_params(out, q, k_cache, v_cache, block_tables, context_lens, scale, sh);
     p.seq_order = seq_order;
     p.window = window;
     p.num_sinks = num_sinks;
-    const long long units = visible_units(p.context_cap, window, num_sinks, 16);
-    const long long parts = window_partitions(units, 16, partition_size);
+    const long long units = visible_units(p.context_cap, window, num_sinks, kInt4Step);
+    const long long parts = window_partitions(units, kInt4Step, partition_size);
     if (parts > INT_MAX) return PA_ERR_UNSUPPORTED;
     st = take_workspace(p, sh, parts, workspace, workspace_bytes, counters, num_counters);
     if (st != PA_OK) return st;
-    p.partition_blocks = parts > 1 ? partition_size / 16 : INT_MAX / 2;
+    p.partition_blocks = parts > 1 ? partition_size / kInt4Step : INT_MAX / 2;
     const dim3 grid(static_cast<unsigned>(std::max(1LL, parts)), num_kv_heads, num_seqs);
     const cudaError_t e = with_variant(dtype, head_dim, block_size, [&](auto tt, auto dd, auto bb) -> cudaError_t {
         using T = typename decltype(tt)::type;
@@ -1290,7 +1299,11 @@ pa_status pa_decode_int4(void* out, const void* q, const void* k_cache, const vo
         if constexpr (pa::IsF32<T>::value) {
             return cudaErrorInvalidValue;
         } else {
-            return launch_early(pa::pa_decode_int4_kernel<T, kD, kB, kInt4Warps>, grid, dim3(kInt4Warps * 32), 0,
+            auto kernel = pa::pa_decode_int4_kernel<T, kD, kB, PA_INT4_WARPS, kInt4Stages<kD>>;
+            const cudaError_t fit = ensure_smem(reinterpret_cast<const void*>(kernel));
+            if (fit != cudaSuccess) return fit;
+            return launch_early(kernel, grid, dim3(PA_INT4_WARPS * 32),
+                                pa::Int4Smem<kD, kB, PA_INT4_WARPS, kInt4Stages<kD>>::kTotal,
                                 static_cast<cudaStream_t>(stream), PA_EARLY_LAUNCH, p);
         }
     });

@@ -18,9 +18,10 @@
 // eight dims of a 16-dim tile) in the output rows.  A word of a tile is then a
 // whole operand of one MMA in five operations.
 //
-// The words lie in HBM in operand order, so a lane loads its own 16-byte
-// vectors straight into registers: no staging in shared memory, no barriers,
-// and the next units' loads stay in flight under the present one's arithmetic.
+// Each warp takes steps of 32 tokens (one online-softmax step each) from a
+// ring of shared-memory stages of its own, filled by bulk copies of whole
+// (block, head) tiles, K and V, codes and group words together; the words lie
+// in operand order, so a lane reads its own 16-byte vectors.
 //
 // Statistics: fp32 running reference and sum in base 2.  The reference moves
 // only when a score exceeds it by 2^8 (one vote a unit instead of a reduction
@@ -87,73 +88,60 @@ __device__ __forceinline__ int load_q_int4(uint32_t (&qa)[D / 16][2], float (&su
     return shift;
 }
 
-// Loads of data read once: past L1, first out of L2.
-__device__ __forceinline__ uint4 ldg_stream16(const uint8_t* p, uint64_t policy) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p), "l"(policy));
-    return v;
-}
-__device__ __forceinline__ uint2 ldg_stream8(const uint8_t* p, uint64_t policy) {
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v2.u32 {%0,%1}, [%2], %3;"
-                 : "=r"(v.x), "=r"(v.y)
-                 : "l"(p), "l"(policy));
-    return v;
-}
-__device__ __forceinline__ uint32_t ldg_stream4(const uint8_t* p, uint64_t policy) {
-    uint32_t v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.u32 %0, [%1], %2;" : "=r"(v) : "l"(p), "l"(policy));
-    return v;
-}
-
-// The tokens a decode attends to, in units of 16: with a window, the units of
+// The tokens a decode attends to, in steps of 32: with a window, the steps of
 // the first num_sinks tokens and those from position L - window on.
-struct VisibleUnits {
+struct VisibleSteps {
     int L, wlo, sinks;   // token t is visible iff t < L and (t >= wlo or t < sinks)
-    int first, gap, n;   // n units: 0 .. first - 1, then first + gap ..
-    __device__ __forceinline__ VisibleUnits(int len, int window, int num_sinks) {
+    int first, gap, n;   // n steps: 0 .. first - 1, then first + gap ..
+    __device__ __forceinline__ VisibleSteps(int len, int window, int num_sinks) {
         L = len;
         wlo = window > 0 && len > window ? len - window : 0;
         sinks = min(num_sinks, len);
-        const int units = (len + 15) >> 4, wu = wlo >> 4, su = (sinks + 15) >> 4;
-        first = wu > su ? su : units;
-        gap = wu > su ? wu - su : 0;
-        n = units - gap;
+        const int all = (len >> 5) + ((len & 31) != 0), ws = wlo >> 5, ss = (sinks >> 5) + ((sinks & 31) != 0);
+        first = ws > ss ? ss : all;
+        gap = ws > ss ? ws - ss : 0;
+        n = all - gap;
     }
-    __device__ __forceinline__ int unit(int i) const { return i < first ? i : i + gap; }
+    __device__ __forceinline__ int step(int i) const { return i < first ? i : i + gap; }
     __device__ __forceinline__ bool token(int t) const { return t < L && (t >= wlo || t < sinks); }
-    // whether [t, t + 16) is visible whole
-    __device__ __forceinline__ bool whole(int t) const { return t + 16 <= L && (t >= wlo || t + 16 <= sinks); }
-    // whether any of [t, t + n) is visible
-    __device__ __forceinline__ bool any(int t, int n) const { return t < L && (t + n > wlo || t < sinks); }
+    // whether the n tokens from t on are visible, all of them or any
+    __device__ __forceinline__ bool whole(int t, int n) const { return L - t >= n && (t >= wlo || sinks - t >= n); }
+    __device__ __forceinline__ bool any(int t, int n) const { return t < L && (wlo - t < n || t < sinks); }
 };
 
-// One unit's words: K and V codes (per 64 dims; 8-token blocks: two words of
-// the unit's first block, two of its second) and the group words of tokens r
-// and r + 8.
-template <int D>
-struct UnitInt4 {
-    uint4 k[D / 64], v[D / 64];
-    uint32_t kw[2][D / 64], vw[2][D / 64];
-    int ok;   // bit 0, 1: the block of tokens 0..7, 8..15 of the unit may be read
+template <int D, int B, int NW, int ST>
+struct Int4Smem {
+    static constexpr int kTile = int4_tile_bytes(B, D);
+    static constexpr int kBlocks = 32 / B;                 // blocks of a step
+    static constexpr int kStage = 2 * kBlocks * kTile;     // their K tiles, then their V tiles
+    static constexpr int kRing = NW * ST * kStage;
+    static constexpr int kMerge = NW * kMaxGroup * (kMergeRow<D> + 2) * 4;   // in the ring's place, after it
+    static constexpr int kArea = kRing > kMerge ? kRing : kMerge;
+    static constexpr int kTotal = kArea + NW * ST * 8;
+    static_assert(kTile % 16 == 0 && kArea % 8 == 0, "bulk copies move 16-byte units; barriers are 8-byte words");
 };
 
-template <typename T, int D, int B, int NW>
-__global__ void __launch_bounds__(NW * 32, (D == 64 ? 16 : 12) / NW)
+template <typename T, int D, int B, int NW, int ST>
+__global__ void __launch_bounds__(NW * 32, 16 / NW)
     pa_decode_int4_kernel(const __grid_constant__ DecodeParams p) {
+    using Sm = Int4Smem<D, B, NW, ST>;
     constexpr int NC = D / 64;                   // groups of a row
-    constexpr int kTile = int4_tile_bytes(B, D);
-    constexpr int kCodes = B * D / 2;
-    constexpr int kDepth = 2;                    // units loaded ahead
-    __shared__ float mo[NW * kMaxGroup * kMergeRow<D>];
-    __shared__ float mml[NW * kMaxGroup * 2];
+    constexpr int kTile = Sm::kTile, kCodes = B * D / 2;
+    constexpr int NB = Sm::kBlocks, kSpan = 32 / NB;   // blocks of a step; steps whose ids a warp holds at once
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int last_arrival;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
     const int part = blockIdx.x, kvh = blockIdx.y;
     int s = blockIdx.z;
+    uint8_t* ring = smem + warp * ST * Sm::kStage;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sm::kArea) + warp * ST;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < ST; ++i) mbar_init(&bars[i], 1);
+        fence_barrier_init();
+    }
+    __syncwarp();
     wait_for_prior_work();
     if (p.seq_order != nullptr) {
         s = __ldg(p.seq_order + blockIdx.z);
@@ -169,95 +157,58 @@ __global__ void __launch_bounds__(NW * 32, (D == 64 ? 16 : 12) / NW)
         L = L < 0 ? 0 : p.context_cap;
     }
     T* out = reinterpret_cast<T*>(p.out) + (static_cast<long long>(s) * p.num_q_heads + kvh * group) * D;
-    const VisibleUnits vis(L, p.window, p.num_sinks);
+    const VisibleSteps vis(L, p.window, p.num_sinks);
     const int u0 = part * p.partition_blocks;
     if (u0 >= vis.n) {
         if (part == 0)   // an empty context
             for (int i = threadIdx.x; i < group * D; i += NW * 32) out[i] = from_float<T>(0.f);
         return;
     }
-    const int nu = min(vis.n - u0, p.partition_blocks);          // this CTA's units
+    const int nu = min(vis.n - u0, p.partition_blocks);          // this CTA's steps
     const int n_w = nu > warp ? (nu - warp + NW - 1) / NW : 0;   // this warp's: u0 + warp, + NW, ..
+    auto first_token = [&](int i) -> int { return 32 * vis.step(u0 + warp + i * NW); };
 
+    // Block ids, kSpan steps at a time: lane = (step % kSpan) * NB + block of the step
     const int32_t* table = p.block_tables + static_cast<long long>(s) * p.max_blocks_per_seq;
-    // ids of the blocks under this warp's unit i, 32 units at a time, lane = i % 32
-    auto load_id = [&](int i, int half) -> int {
+    auto load_ids = [&](int span) -> int {
+        const int i = span * kSpan + lane / NB;
         if (i >= n_w) return -1;
-        const int t = 16 * vis.unit(u0 + warp + i * NW) + (B == 8 ? 8 * half : 0);
-        if (!vis.any(t, B == 8 ? 8 : 16)) return -1;
+        const int t = first_token(i) + lane % NB * B;
+        if (!vis.any(t, B)) return -1;
         const int id = __ldg(table + t / B);
         if (id >= 0 && static_cast<long long>(id) < p.num_blocks) return id;
         flag_error(1 /* PA_DEVERR_BLOCK_ID */);
         return -1;
     };
-    int ids[2], ids8[2] = {-1, -1};   // two windows of 32 units (8-token blocks: and the units' second blocks)
-    ids[0] = load_id(lane, 0);
-    ids[1] = load_id(32 + lane, 0);
-    if constexpr (B == 8) {
-        ids8[0] = load_id(lane, 1);
-        ids8[1] = load_id(32 + lane, 1);
-    }
-    int window0 = 0;   // first unit of ids[0]
+    int ids0 = load_ids(0), ids1 = load_ids(1);
+    int span = 0;   // of ids0
 
     const uint64_t policy = l2_evict_first_policy();
     const uint8_t* kpool = reinterpret_cast<const uint8_t*>(p.k_cache);
     const uint8_t* vpool = reinterpret_cast<const uint8_t*>(p.v_cache);
-    auto fetch = [&](UnitInt4<D>& f, int i) {   // warp-uniform i
-        const int w = (i - window0) >> 5;
-        const int id = __shfl_sync(0xffffffffu, w ? ids[1] : ids[0], i & 31);
-        if constexpr (B == 8) {
-            const int id8 = __shfl_sync(0xffffffffu, w ? ids8[1] : ids8[0], i & 31);
-            f.ok = (id >= 0 ? 1 : 0) | (id8 >= 0 ? 2 : 0);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int b = h ? id8 : id;
-                const long long at = (static_cast<long long>(b < 0 ? 0 : b) * p.num_kv_heads + kvh) * kTile;
-#pragma unroll
-                for (int ch = 0; ch < NC; ++ch) {
-                    uint2 k = make_uint2(0u, 0u), v = make_uint2(0u, 0u);
-                    f.kw[h][ch] = f.vw[h][ch] = 0u;
-                    if (b >= 0) {
-                        k = ldg_stream8(kpool + at + (ch * 32 + lane) * 8, policy);
-                        v = ldg_stream8(vpool + at + (ch * 32 + lane) * 8, policy);
-                        f.kw[h][ch] = ldg_stream4(kpool + at + kCodes + (r * NC + ch) * 4, policy);
-                        f.vw[h][ch] = ldg_stream4(vpool + at + kCodes + (r * NC + ch) * 4, policy);
-                    }
-                    if (h == 0) {
-                        f.k[ch].x = k.x; f.k[ch].y = k.y; f.v[ch].x = v.x; f.v[ch].y = v.y;
-                    } else {
-                        f.k[ch].z = k.x; f.k[ch].w = k.y; f.v[ch].z = v.x; f.v[ch].w = v.y;
-                    }
-                }
-            }
-        } else {
-            f.ok = id >= 0 ? 3 : 0;
-            if (id >= 0) {
-                const int tg = B == 32 ? (vis.unit(u0 + warp + i * NW) & 1) : 0;
-                const long long at = (static_cast<long long>(id) * p.num_kv_heads + kvh) * kTile;
-#pragma unroll
-                for (int ch = 0; ch < NC; ++ch) {
-                    f.k[ch] = ldg_stream16(kpool + at + ((tg * NC + ch) * 32 + lane) * 16, policy);
-                    f.v[ch] = ldg_stream16(vpool + at + ((tg * NC + ch) * 32 + lane) * 16, policy);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const long long w0 = at + kCodes + (16 * tg + r + 8 * h) * NC * 4;
-                    if constexpr (NC == 2) {
-                        const uint2 k = ldg_stream8(kpool + w0, policy), v = ldg_stream8(vpool + w0, policy);
-                        f.kw[h][0] = k.x; f.kw[h][1] = k.y; f.vw[h][0] = v.x; f.vw[h][1] = v.y;
-                    } else {
-                        f.kw[h][0] = ldg_stream4(kpool + w0, policy);
-                        f.vw[h][0] = ldg_stream4(vpool + w0, policy);
-                    }
-                }
-            }
+    // the id of block lane % NB of step i (of the spans held)
+    auto step_id = [&](int i) -> int {
+        const int from = i % kSpan * NB + lane % NB;
+        const int a = __shfl_sync(0xffffffffu, ids0, from), b = __shfl_sync(0xffffffffu, ids1, from);
+        return i / kSpan == span ? a : b;
+    };
+    auto issue = [&](int i) {
+        const int id = step_id(i);
+        const uint32_t ok = __ballot_sync(0xffffffffu, lane < NB && id >= 0);
+#ifdef PA_TEST_HOOKS
+        if (g_test_skip_first_copy && i == 0 && warp == 0 && s == 0 && kvh == 0 && part == 0) return;
+#endif
+        uint64_t* bar = &bars[i % ST];
+        uint8_t* dst = ring + i % ST * Sm::kStage;
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(ok) * 2 * kTile);
+        if (lane < NB && id >= 0) {
+            const long long at = (static_cast<long long>(id) * p.num_kv_heads + kvh) * kTile;
+            bulk_copy_g2s(dst + lane * kTile, kpool + at, kTile, bar, policy);
+            bulk_copy_g2s(dst + (NB + lane) * kTile, vpool + at, kTile, bar, policy);
         }
     };
-
-    UnitInt4<D> f[kDepth];
-#pragma unroll
-    for (int k = 0; k < kDepth; ++k)
-        if (k < n_w) fetch(f[k], k);
+    int issued = min(n_w, ST);
+    for (int i = 0; i < issued; ++i) issue(i);
 
     uint32_t qa[D / 16][2];
     float qsum[NC][2];
@@ -280,46 +231,96 @@ __global__ void __launch_bounds__(NW * 32, (D == 64 ? 16 : 12) / NW)
 #pragma unroll
     for (int ch = 0; ch < NC; ++ch) zo[ch][0] = zo[ch][1] = 0.f;
 
-    // the operand words of MMA m of chunk ch, from the unit's words
-    auto word = [&](const uint4& x, int m) -> uint32_t {
-        if constexpr (B == 8) {
-            const uint32_t a = m < 2 ? x.x : x.y, b = m < 2 ? x.z : x.w;
-            return __byte_perm(a, b, (m & 1) ? 0x7351 : 0x6240);
+    // The four operand words of 16 tokens (half g of the step) and chunk ch,
+    // and the group words of token 8 h + r, from the tiles at `base`.
+    auto words = [&](uint32_t base, int g, int ch, uint32_t (&w)[4]) {
+        if constexpr (B == 8) {   // two blocks of two words; bytes of the two alternate in an operand word
+            const uint2 a = lds64(base + 2 * g * kTile + (ch * 32 + lane) * 8);
+            const uint2 b = lds64(base + (2 * g + 1) * kTile + (ch * 32 + lane) * 8);
+            w[0] = __byte_perm(a.x, b.x, 0x6240);
+            w[1] = __byte_perm(a.x, b.x, 0x7351);
+            w[2] = __byte_perm(a.y, b.y, 0x6240);
+            w[3] = __byte_perm(a.y, b.y, 0x7351);
         } else {
-            return m == 0 ? x.x : (m == 1 ? x.y : (m == 2 ? x.z : x.w));
+            const uint4 a = lds128(base + (B == 16 ? g * kTile + (ch * 32 + lane) * 16 : ((g * NC + ch) * 32 + lane) * 16));
+            w[0] = a.x;
+            w[1] = a.y;
+            w[2] = a.z;
+            w[3] = a.w;
+        }
+    };
+    auto group_words = [&](uint32_t base, int h, uint32_t (&w)[NC]) {
+        const uint32_t at = base + 8 * h / B * kTile + kCodes + (8 * h % B + r) * NC * 4;
+        if constexpr (NC == 2) {
+            const uint2 a = lds64(at);
+            w[0] = a.x;
+            w[1] = a.y;
+        } else {
+            w[0] = lds32(at);
         }
     };
 
-    auto compute = [&](const UnitInt4<D>& u, int i) {
-        // S^T of codes, per group of dims
-        float sc[NC][4];
+    bool failed = false;
+    int i = 0;
+    for (; i < n_w; ++i) {
+        if (i / kSpan != span) {
+            ++span;
+            ids0 = ids1;
+            ids1 = load_ids(span + 1);
+        }
+        // (the whole warp gives up or none of it: shuffles follow)
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[i % ST], (i / ST) & 1, wait_limit_ns()))) {
+            failed = true;
+            break;
+        }
+        const uint32_t kbase = smem_u32(ring + i % ST * Sm::kStage), vbase = kbase + NB * kTile;
+        const int t0 = first_token(i);
+        const int id = step_id(i);   // (a shuffle: every lane takes part)
+        const uint32_t ok = __ballot_sync(0xffffffffu, lane < NB && id >= 0);
+        const bool whole = ok == (1u << NB) - 1u && vis.whole(t0, 32);
+
+        // S^T of codes, per group of dims; scores x[2h], x[2h + 1] of token 8 h + r and heads 2c, 2c + 1
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+        float sc[2][NC][4];
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch) {
-            sc[ch][0] = sc[ch][1] = sc[ch][2] = sc[ch][3] = 0.f;
+            uint32_t wa[4], wb[4];
+            words(kbase, 0, ch, wa);
+            words(kbase, 1, ch, wb);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[0][ch][e] = sc[1][ch][e] = 0.f;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const uint32_t x = word(u.k[ch], m), y = x >> 8;
-                Mma<__half>::k16(sc[ch], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u,
+                const uint32_t a = wa[m], a8 = a >> 8, b = wb[m], b8 = b >> 8;
+                Mma<__half>::k16(sc[0][ch], a & 0x000f000fu, a8 & 0x000f000fu, a & 0x00f000f0u, a8 & 0x00f000f0u,
+                                 qa[4 * ch + m][0], qa[4 * ch + m][1]);
+                Mma<__half>::k16(sc[1][ch], b & 0x000f000fu, b8 & 0x000f000fu, b & 0x00f000f0u, b8 & 0x00f000f0u,
                                  qa[4 * ch + m][0], qa[4 * ch + m][1]);
             }
         }
-        float x[4] = {0.f, 0.f, 0.f, 0.f};   // scores: (token r, head 2c), (r, 2c + 1), (r + 8, 2c), (r + 8, 2c + 1)
-        float vs[2][NC], vz[2][NC];
-        const int t0 = 16 * vis.unit(u0 + warp + i * NW) + r;
-        const bool whole = u.ok == 3 && vis.whole(t0 - r);
+        float vs[4][NC], vz[4][NC];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 4; ++h) {
+            uint32_t kw[NC], vw[NC];
+            group_words(kbase, h, kw);
+            group_words(vbase, h, vw);
 #pragma unroll
             for (int ch = 0; ch < NC; ++ch) {
-                const float ks = __uint_as_float(u.kw[h][ch] << 16) * code_scale;
-                const float kz = __uint_as_float(u.kw[h][ch] & 0xffff0000u);
-                x[2 * h] = fmaf(ks, sc[ch][2 * h], fmaf(kz, qsum[ch][0], x[2 * h]));
-                x[2 * h + 1] = fmaf(ks, sc[ch][2 * h + 1], fmaf(kz, qsum[ch][1], x[2 * h + 1]));
-                vs[h][ch] = __uint_as_float(u.vw[h][ch] << 16);
-                vz[h][ch] = __uint_as_float(u.vw[h][ch] & 0xffff0000u);
+                const float ks = __uint_as_float(kw[ch] << 16) * code_scale;
+                const float kz = __uint_as_float(kw[ch] & 0xffff0000u);
+                const float(&q)[4] = sc[h / 2][ch];
+                x[2 * h] = fmaf(ks, q[2 * (h & 1)], fmaf(kz, qsum[ch][0], x[2 * h]));
+                x[2 * h + 1] = fmaf(ks, q[2 * (h & 1) + 1], fmaf(kz, qsum[ch][1], x[2 * h + 1]));
+                vs[h][ch] = __uint_as_float(vw[ch] << 16);
+                vz[h][ch] = __uint_as_float(vw[ch] & 0xffff0000u);
             }
-            if (!whole) {   // tokens that are not attended, or whose block id was refused: whatever lies there is not used
-                if (!(((u.ok >> h) & 1) && vis.token(t0 + 8 * h))) {
+        }
+        if (!whole) {   // tokens that are not attended, or whose block id was refused: whatever lies there is not used
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                if (!(((ok >> (8 * h / B)) & 1u) && vis.token(t0 + 8 * h + r))) {
                     x[2 * h] = x[2 * h + 1] = kNegInf;
 #pragma unroll
                     for (int ch = 0; ch < NC; ++ch) vs[h][ch] = vz[h][ch] = 0.f;
@@ -327,9 +328,12 @@ __global__ void __launch_bounds__(NW * 32, (D == 64 ? 16 : 12) / NW)
             }
         }
         // the reference of the softmax and the unit of V's scales, moved when they have to be
-        const float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
-        float sm = fmaxf(vs[0][0], vs[1][0]);
-        if constexpr (NC == 2) sm = fmaxf(sm, fmaxf(vs[0][1], vs[1][1]));
+        const float mx0 = fmaxf(fmaxf(x[0], x[2]), fmaxf(x[4], x[6])), mx1 = fmaxf(fmaxf(x[1], x[3]), fmaxf(x[5], x[7]));
+        float sm = 0.f;
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int ch = 0; ch < NC; ++ch) sm = fmaxf(sm, vs[h][ch]);
         if (__any_sync(0xffffffffu, mx0 > m_ref[0] + 8.f || mx1 > m_ref[1] + 8.f || sm > v_most)) {
             float n0 = fmaxf(m_ref[0], mx0), n1 = fmaxf(m_ref[1], mx1);
 #pragma unroll
@@ -344,7 +348,7 @@ __global__ void __launch_bounds__(NW * 32, (D == 64 ? 16 : 12) / NW)
             m_ref[0] = n0;
             m_ref[1] = n1;
             float vu = 1.f;
-            if (sm > v_most) {   // (scales are bf16: at most 2^128; an infinite one makes the output NaN)
+            if (sm > v_most) {   // (scales are bf16: below 2^128; an infinite one makes the output NaN)
                 const int e = static_cast<int>((__float_as_uint(sm) >> 23) & 0xff) - 127;   // sm < 2^(e + 1)
                 int up = 5 - e;                                                             // p * scale <= 2^8 2^7
                 up = up > 126 ? 126 : up;
@@ -369,46 +373,51 @@ __global__ void __launch_bounds__(NW * 32, (D == 64 ? 16 : 12) / NW)
             l_run[1] *= a1;
         }
         const float mu0 = m_ref[0] == kNegInf ? 0.f : m_ref[0], mu1 = m_ref[1] == kNegInf ? 0.f : m_ref[1];
-        const float p0 = exp2_approx(x[0] - mu0), p1 = exp2_approx(x[1] - mu1);
-        const float p2 = exp2_approx(x[2] - mu0), p3 = exp2_approx(x[3] - mu1);
-        l_run[0] += p0 + p2;
-        l_run[1] += p1 + p3;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {   // x becomes p
+            x[2 * h] = exp2_approx(x[2 * h] - mu0);
+            x[2 * h + 1] = exp2_approx(x[2 * h + 1] - mu1);
+        }
+        l_run[0] += (x[0] + x[2]) + (x[4] + x[6]);
+        l_run[1] += (x[1] + x[3]) + (x[5] + x[7]);
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch) {
-            zo[ch][0] = fmaf(p0, vz[0][ch], fmaf(p2, vz[1][ch], zo[ch][0]));
-            zo[ch][1] = fmaf(p1, vz[0][ch], fmaf(p3, vz[1][ch], zo[ch][1]));
-            const float s0 = vs[0][ch] * v_unit, s1 = vs[1][ch] * v_unit;
-            const uint32_t b0 = movmatrix_trans(Mma<__half>::pack(p0 * s0, p1 * s0));
-            const uint32_t b1 = movmatrix_trans(Mma<__half>::pack(p2 * s1, p3 * s1));
+            uint32_t pb[4];   // P^T as the B operand, tokens 8 h ..
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                zo[ch][0] = fmaf(x[2 * h], vz[h][ch], zo[ch][0]);
+                zo[ch][1] = fmaf(x[2 * h + 1], vz[h][ch], zo[ch][1]);
+                const float sv = vs[h][ch] * v_unit;
+                pb[h] = movmatrix_trans(Mma<__half>::pack(x[2 * h] * sv, x[2 * h + 1] * sv));
+            }
+            uint32_t wa[4], wb[4];
+            words(vbase, 0, ch, wa);
+            words(vbase, 1, ch, wb);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const uint32_t w = word(u.v[ch], m), y = w >> 8;
-                Mma<__half>::k16(o[4 * ch + m], w & 0x000f000fu, w & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u,
-                                 b0, b1);
+                const uint32_t a = wa[m], a8 = a >> 8, b = wb[m], b8 = b >> 8;
+                Mma<__half>::k16(o[4 * ch + m], a & 0x000f000fu, a & 0x00f000f0u, a8 & 0x000f000fu, a8 & 0x00f000f0u,
+                                 pb[0], pb[1]);
+                Mma<__half>::k16(o[4 * ch + m], b & 0x000f000fu, b & 0x00f000f0u, b8 & 0x000f000fu, b8 & 0x00f000f0u,
+                                 pb[2], pb[3]);
             }
         }
-    };
-
-    for (int i = 0; i < n_w; i += kDepth) {
-        if (i - window0 >= 32) {   // (kDepth divides 32: a window starts at an i of this loop)
-            window0 += 32;
-            ids[0] = ids[1];
-            ids[1] = load_id(window0 + 32 + lane, 0);
-            if constexpr (B == 8) {
-                ids8[0] = ids8[1];
-                ids8[1] = load_id(window0 + 32 + lane, 1);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kDepth; ++k) {
-            if (i + k < n_w) {
-                compute(f[k], i + k);
-                if (i + k + kDepth < n_w) fetch(f[k], i + k + kDepth);
-            }
+        __syncwarp();   // every lane has read the stage
+        if (i + ST < n_w) {
+            issue(i + ST);
+            ++issued;
         }
     }
+    if (failed) {
+        if (lane == 0) flag_error(8 /* PA_DEVERR_TIMEOUT */);
+        // let the copies already in flight land before the CTA may exit
+        for (int k = i; k < issued; ++k) mbar_wait_bounded(&bars[k % ST], (k / ST) & 1, wait_limit_ns());
+    }
+    const int any_failed = __syncthreads_or(failed ? 1 : 0);   // (the ring is free now)
 
     // ---- this warp's state in true units, then the warps' merge
+    float* mo = reinterpret_cast<float*>(smem);
+    float* mml = mo + NW * kMaxGroup * kMergeRow<D>;
     const float back = v_unit > 0.f ? 16777216.f / v_unit : 0.f;   // 2^24 / unit
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -427,8 +436,11 @@ __global__ void __launch_bounds__(NW * 32, (D == 64 ? 16 : 12) / NW)
                 row[16 * mt + 8 + r] = fmaf(o[mt][2 + e], back * 0.0625f, zo[mt / 4][e]);
             }
             if (r == 0) {
-                mml[(warp * kMaxGroup + h) * 2] = m_ref[e];
-                mml[(warp * kMaxGroup + h) * 2 + 1] = l_run[e];
+                // a warp whose copies timed out counts as one without tokens: the
+                // call's outputs are not the attention then, but no merge reads
+                // what an earlier call left in the workspace
+                mml[(warp * kMaxGroup + h) * 2] = any_failed ? kNegInf : m_ref[e];
+                mml[(warp * kMaxGroup + h) * 2 + 1] = any_failed ? 0.f : l_run[e];
             }
         }
     }

@@ -137,8 +137,8 @@ def test_plans(lib):
     assert ops.pa_decode_int4_plan(3, 8, 2, 64, 1000, partition_size=128) == (128, 3 * 8 * 8 * 66 * 4)
     assert ops.pa_decode_int4_plan(3, 8, 2, 64, 1000, partition_size=0) == (0, 0)
     assert ops.pa_decode_int4_plan(3, 8, 2, 64, 0, partition_size=128) == (128, 0)
-    # a window of 100 touches 8 units of 16 at most, 20 first tokens two more: 10 units, 5 of 32 tokens
-    assert ops.pa_decode_int4_plan(3, 8, 2, 64, 1000, 100, 20, 32) == (32, 3 * 8 * 5 * 66 * 4)
+    # a window of 100 touches 5 steps of 32 tokens at most, 20 first tokens one more; 8 and 2 blocks of 16
+    assert ops.pa_decode_int4_plan(3, 8, 2, 64, 1000, 100, 20, 32) == (32, 3 * 8 * 6 * 66 * 4)
     assert ops.pa_decode_window_plan(3, 8, 2, 64, 16, 1000, 100, 20, 32) == (32, 3 * 8 * 5 * 66 * 4)
     assert ops.pa_decode_window_plan(3, 8, 2, 64, 16, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 1 << 20)[1] > 0
     for bad in ((-1, 8, 2, 64, 16, 100, 10), (3, 8, 2, 64, 16, 100, 0), (3, 8, 2, 64, 16, 100, 10, -1),
