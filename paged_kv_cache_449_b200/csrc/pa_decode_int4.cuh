@@ -19,9 +19,11 @@
 // whole operand of one MMA in five operations.
 //
 // Each warp takes steps of 32 tokens (one online-softmax step each) from a
-// ring of shared-memory stages of its own, filled by bulk copies of whole
-// (block, head) tiles, K and V, codes and group words together; the words lie
-// in operand order, so a lane reads its own 16-byte vectors.
+// ring of shared-memory stages of its own, filled by asynchronous 16-byte
+// copies of each (block, head) tile, codes and group words; the words lie in
+// operand order, so a lane reads its own 16-byte vectors.  (Bulk copies of
+// whole tiles, issued by one lane per block, cost about a fifth of the
+// kernel's instructions.)
 //
 // Statistics: fp32 running reference and sum in base 2.  The reference moves
 // only when a score exceeds it by 2^8 (one vote a unit instead of a reduction
@@ -88,6 +90,15 @@ __device__ __forceinline__ int load_q_int4(uint32_t (&qa)[D / 16][2], float (&su
     return shift;
 }
 
+// D(16x8 f32) = A(16x16 fp16) B(16x8 fp16) + C; not volatile: the compiler may
+// place it as it likes.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        const uint32_t (&b)[2], float c0, float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
 // The tokens a decode attends to, in steps of 32: with a window, the steps of
 // the first num_sinks tokens and those from position L - window on.
 struct VisibleSteps {
@@ -117,8 +128,8 @@ struct Int4Smem {
     static constexpr int kRing = NW * ST * kStage;
     static constexpr int kMerge = NW * kMaxGroup * (kMergeRow<D> + 2) * 4;   // in the ring's place, after it
     static constexpr int kArea = kRing > kMerge ? kRing : kMerge;
-    static constexpr int kTotal = kArea + NW * ST * 8;
-    static_assert(kTile % 16 == 0 && kArea % 8 == 0, "bulk copies move 16-byte units; barriers are 8-byte words");
+    static constexpr int kTotal = kArea;
+    static_assert(kTile % 16 == 0, "copies move 16-byte units");
 };
 
 template <typename T, int D, int B, int NW, int ST>
@@ -134,14 +145,7 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
     const int r = lane >> 2, c = lane & 3;
     const int part = blockIdx.x, kvh = blockIdx.y;
     int s = blockIdx.z;
-    uint8_t* ring = smem + warp * ST * Sm::kStage;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sm::kArea) + warp * ST;
-    if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < ST; ++i) mbar_init(&bars[i], 1);
-        fence_barrier_init();
-    }
-    __syncwarp();
+    const uint8_t* ring = smem + warp * ST * Sm::kStage;
     wait_for_prior_work();
     if (p.seq_order != nullptr) {
         s = __ldg(p.seq_order + blockIdx.z);
@@ -170,45 +174,61 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
 
     // Block ids, kSpan steps at a time: lane = (step % kSpan) * NB + block of the step
     const int32_t* table = p.block_tables + static_cast<long long>(s) * p.max_blocks_per_seq;
+    bool refused = false;   // whether any id so far was (the whole warp knows)
     auto load_ids = [&](int span) -> int {
         const int i = span * kSpan + lane / NB;
-        if (i >= n_w) return -1;
-        const int t = first_token(i) + lane % NB * B;
-        if (!vis.any(t, B)) return -1;
-        const int id = __ldg(table + t / B);
-        if (id >= 0 && static_cast<long long>(id) < p.num_blocks) return id;
-        flag_error(1 /* PA_DEVERR_BLOCK_ID */);
-        return -1;
+        int id = -1;
+        bool bad = false;
+        if (i < n_w) {
+            const int t = first_token(i) + lane % NB * B;
+            if (vis.any(t, B)) {
+                id = __ldg(table + t / B);
+                bad = id < 0 || static_cast<long long>(id) >= p.num_blocks;
+                if (bad) {
+                    flag_error(1 /* PA_DEVERR_BLOCK_ID */);
+                    id = -1;
+                }
+            }
+        }
+        refused = refused || __any_sync(0xffffffffu, bad);
+        return id;
     };
     int ids0 = load_ids(0), ids1 = load_ids(1);
     int span = 0;   // of ids0
 
+    // Copies of step i (of the spans held) into its stage: for each tile the
+    // codes, 16 bytes a lane, and the group words of all tiles, 16 bytes a
+    // lane too.  A block that is not attended or whose id was refused is left out.
     const uint64_t policy = l2_evict_first_policy();
-    const uint8_t* kpool = reinterpret_cast<const uint8_t*>(p.k_cache);
-    const uint8_t* vpool = reinterpret_cast<const uint8_t*>(p.v_cache);
-    // the id of block lane % NB of step i (of the spans held)
-    auto step_id = [&](int i) -> int {
-        const int from = i % kSpan * NB + lane % NB;
-        const int a = __shfl_sync(0xffffffffu, ids0, from), b = __shfl_sync(0xffffffffu, ids1, from);
-        return i / kSpan == span ? a : b;
+    const uint32_t stride = static_cast<uint32_t>(p.num_kv_heads) * kTile;
+    const uint8_t* kcodes = reinterpret_cast<const uint8_t*>(p.k_cache) + static_cast<long long>(kvh) * kTile + lane * 16;
+    const uint8_t* vcodes = reinterpret_cast<const uint8_t*>(p.v_cache) + static_cast<long long>(kvh) * kTile + lane * 16;
+    constexpr int PL = B * NC / 4;            // lanes that hold a tile's group words
+    const int wt = lane / PL;                 // the tile whose words this lane copies: K's blocks, then V's
+    const int word_off = kCodes + lane % PL * 16;
+    const uint8_t* wsrc = (wt < NB ? kcodes : vcodes) - lane * 16 + word_off;
+    const uint32_t code_dst = smem_u32(ring) + lane * 16, word_dst = smem_u32(ring) + wt * kTile + word_off;
+    auto step_id = [&](int i, int block) -> int {   // (a shuffle: the whole warp calls it)
+        return __shfl_sync(0xffffffffu, i / kSpan == span ? ids0 : ids1, i % kSpan * NB + block);
     };
-    auto issue = [&](int i) {
-        const int id = step_id(i);
-        const uint32_t ok = __ballot_sync(0xffffffffu, lane < NB && id >= 0);
-#ifdef PA_TEST_HOOKS
-        if (g_test_skip_first_copy && i == 0 && warp == 0 && s == 0 && kvh == 0 && part == 0) return;
-#endif
-        uint64_t* bar = &bars[i % ST];
-        uint8_t* dst = ring + i % ST * Sm::kStage;
-        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(ok) * 2 * kTile);
-        if (lane < NB && id >= 0) {
-            const long long at = (static_cast<long long>(id) * p.num_kv_heads + kvh) * kTile;
-            bulk_copy_g2s(dst + lane * kTile, kpool + at, kTile, bar, policy);
-            bulk_copy_g2s(dst + (NB + lane) * kTile, vpool + at, kTile, bar, policy);
+    auto at = [&](const uint8_t* base, int id) { return base + static_cast<uint64_t>(static_cast<uint32_t>(id)) * stride; };
+    auto issue = [&](int i, uint32_t stage) {   // stage: the stage's offset in the ring
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int id = step_id(i, b);
+            if (id >= 0 && (kCodes >= 512 || lane * 16 < kCodes)) {
+                copy_codes<kCodes>(code_dst + stage + b * kTile, at(kcodes, id), policy);
+                copy_codes<kCodes>(code_dst + stage + (NB + b) * kTile, at(vcodes, id), policy);
+            }
         }
+        const int id = step_id(i, wt % NB);
+        if (id >= 0 && wt < 2 * NB) copy16_async<0>(word_dst + stage, at(wsrc, id), policy);
     };
-    int issued = min(n_w, ST);
-    for (int i = 0; i < issued; ++i) issue(i);
+#pragma unroll
+    for (int i = 0; i < ST; ++i) {
+        if (i < n_w) issue(i, i * Sm::kStage);
+        copy_group_end();
+    }
 
     uint32_t qa[D / 16][2];
     float qsum[NC][2];
@@ -223,7 +243,8 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
 
     float o[D / 16][4];      // O^T of codes: (d = 16 mt + r, h = 2c), (d, 2c + 1), (d + 8, 2c) x 16, (d + 8, 2c + 1) x 16
     float zo[NC][2];         // sum of p * zero, this lane's tokens
-    float m_ref[2] = {kNegInf, kNegInf}, l_run[2] = {0.f, 0.f};
+    float m_ref[2] = {0.f, 0.f}, l_run[2] = {0.f, 0.f};
+    bool started = false;    // whether a token has been attended: m_ref is a score then
     float v_unit = 0.f;      // scales of V are multiplied by this power of two (0: none seen yet)
     float v_most = 0.f;      // the largest scale that v_unit allows
 #pragma unroll
@@ -233,56 +254,56 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
 
     // The four operand words of 16 tokens (half g of the step) and chunk ch,
     // and the group words of token 8 h + r, from the tiles at `base`.
-    auto words = [&](uint32_t base, int g, int ch, uint32_t (&w)[4]) {
+    auto words = [&](const uint8_t* base, int g, int ch, uint32_t (&w)[4]) {
         if constexpr (B == 8) {   // two blocks of two words; bytes of the two alternate in an operand word
-            const uint2 a = lds64(base + 2 * g * kTile + (ch * 32 + lane) * 8);
-            const uint2 b = lds64(base + (2 * g + 1) * kTile + (ch * 32 + lane) * 8);
+            const uint2 a = *reinterpret_cast<const uint2*>(base + 2 * g * kTile + (ch * 32 + lane) * 8);
+            const uint2 b = *reinterpret_cast<const uint2*>(base + (2 * g + 1) * kTile + (ch * 32 + lane) * 8);
             w[0] = __byte_perm(a.x, b.x, 0x6240);
             w[1] = __byte_perm(a.x, b.x, 0x7351);
             w[2] = __byte_perm(a.y, b.y, 0x6240);
             w[3] = __byte_perm(a.y, b.y, 0x7351);
         } else {
-            const uint4 a = lds128(base + (B == 16 ? g * kTile + (ch * 32 + lane) * 16 : ((g * NC + ch) * 32 + lane) * 16));
+            const uint4 a = *reinterpret_cast<const uint4*>(
+                base + (B == 16 ? g * kTile + (ch * 32 + lane) * 16 : ((g * NC + ch) * 32 + lane) * 16));
             w[0] = a.x;
             w[1] = a.y;
             w[2] = a.z;
             w[3] = a.w;
         }
     };
-    auto group_words = [&](uint32_t base, int h, uint32_t (&w)[NC]) {
-        const uint32_t at = base + 8 * h / B * kTile + kCodes + (8 * h % B + r) * NC * 4;
+    auto group_words = [&](const uint8_t* base, int h, uint32_t (&w)[NC]) {
+        const uint8_t* at = base + 8 * h / B * kTile + kCodes + (8 * h % B + r) * NC * 4;
         if constexpr (NC == 2) {
-            const uint2 a = lds64(at);
+            const uint2 a = *reinterpret_cast<const uint2*>(at);
             w[0] = a.x;
             w[1] = a.y;
         } else {
-            w[0] = lds32(at);
+            w[0] = *reinterpret_cast<const uint32_t*>(at);
         }
     };
 
-    bool failed = false;
-    int i = 0;
-    for (; i < n_w; ++i) {
+    uint32_t stage = 0;   // offset of step i's stage
+    for (int i = 0; i < n_w; ++i) {
         if (i / kSpan != span) {
             ++span;
             ids0 = ids1;
             ids1 = load_ids(span + 1);
         }
-        // (the whole warp gives up or none of it: shuffles follow)
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[i % ST], (i / ST) & 1, wait_limit_ns()))) {
-            failed = true;
-            break;
-        }
-        const uint32_t kbase = smem_u32(ring + i % ST * Sm::kStage), vbase = kbase + NB * kTile;
+        copy_groups_wait<ST - 1>();   // this lane's copies of the step; then every lane's
+        __syncwarp();
+        const uint8_t* kbase = ring + stage;
+        const uint8_t* vbase = kbase + NB * kTile;
         const int t0 = first_token(i);
-        const int id = step_id(i);   // (a shuffle: every lane takes part)
-        const uint32_t ok = __ballot_sync(0xffffffffu, lane < NB && id >= 0);
-        const bool whole = ok == (1u << NB) - 1u && vis.whole(t0, 32);
+        const bool whole = vis.whole(t0, 32) && !refused;
 
         // S^T of codes, per group of dims; scores x[2h], x[2h + 1] of token 8 h + r and heads 2c, 2c + 1
+        // relative to the softmax's reference
         float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+        for (int h = 0; h < 4; ++h) {
+            x[2 * h] = -m_ref[0];
+            x[2 * h + 1] = -m_ref[1];
+        }
         float sc[2][NC][4];
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch) {
@@ -290,14 +311,15 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
             words(kbase, 0, ch, wa);
             words(kbase, 1, ch, wb);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[0][ch][e] = sc[1][ch][e] = 0.f;
-#pragma unroll
             for (int m = 0; m < 4; ++m) {
                 const uint32_t a = wa[m], a8 = a >> 8, b = wb[m], b8 = b >> 8;
-                Mma<__half>::k16(sc[0][ch], a & 0x000f000fu, a8 & 0x000f000fu, a & 0x00f000f0u, a8 & 0x00f000f0u,
-                                 qa[4 * ch + m][0], qa[4 * ch + m][1]);
-                Mma<__half>::k16(sc[1][ch], b & 0x000f000fu, b8 & 0x000f000fu, b & 0x00f000f0u, b8 & 0x00f000f0u,
-                                 qa[4 * ch + m][0], qa[4 * ch + m][1]);
+                float(&x0)[4] = sc[0][ch];
+                float(&x1)[4] = sc[1][ch];
+                const bool first = m == 0;
+                mma_f16(x0, a & 0x000f000fu, a8 & 0x000f000fu, a & 0x00f000f0u, a8 & 0x00f000f0u, qa[4 * ch + m],
+                        first ? 0.f : x0[0], first ? 0.f : x0[1], first ? 0.f : x0[2], first ? 0.f : x0[3]);
+                mma_f16(x1, b & 0x000f000fu, b8 & 0x000f000fu, b & 0x00f000f0u, b8 & 0x00f000f0u, qa[4 * ch + m],
+                        first ? 0.f : x1[0], first ? 0.f : x1[1], first ? 0.f : x1[2], first ? 0.f : x1[3]);
             }
         }
         float vs[4][NC], vz[4][NC];
@@ -320,7 +342,7 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
         if (!whole) {   // tokens that are not attended, or whose block id was refused: whatever lies there is not used
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-                if (!(((ok >> (8 * h / B)) & 1u) && vis.token(t0 + 8 * h + r))) {
+                if (!(step_id(i, 8 * h / B) >= 0 && vis.token(t0 + 8 * h + r))) {
                     x[2 * h] = x[2 * h + 1] = kNegInf;
 #pragma unroll
                     for (int ch = 0; ch < NC; ++ch) vs[h][ch] = vz[h][ch] = 0.f;
@@ -334,8 +356,8 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
         for (int h = 0; h < 4; ++h)
 #pragma unroll
             for (int ch = 0; ch < NC; ++ch) sm = fmaxf(sm, vs[h][ch]);
-        if (__any_sync(0xffffffffu, mx0 > m_ref[0] + 8.f || mx1 > m_ref[1] + 8.f || sm > v_most)) {
-            float n0 = fmaxf(m_ref[0], mx0), n1 = fmaxf(m_ref[1], mx1);
+        if (__any_sync(0xffffffffu, mx0 > 8.f || mx1 > 8.f || sm > v_most) || !started) {
+            float n0 = mx0, n1 = mx1;   // by how much the references rise
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
                 n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
@@ -343,10 +365,19 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
             }
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) sm = fmaxf(sm, __shfl_xor_sync(0xffffffffu, sm, off));
-            const float a0 = n0 == kNegInf ? 1.f : exp2_approx(m_ref[0] - n0);
-            const float a1 = n1 == kNegInf ? 1.f : exp2_approx(m_ref[1] - n1);
-            m_ref[0] = n0;
-            m_ref[1] = n1;
+            const bool any = __any_sync(0xffffffffu, n0 != kNegInf);   // (a step masks all heads alike)
+            n0 = !any ? 0.f : (started ? fmaxf(n0, 0.f) : n0);
+            n1 = !any ? 0.f : (started ? fmaxf(n1, 0.f) : n1);
+            // (before the start there is nothing to rescale, and n may be far below zero)
+            const float a0 = started ? exp2_approx(-n0) : 1.f, a1 = started ? exp2_approx(-n1) : 1.f;
+            started = started || any;
+            m_ref[0] += n0;
+            m_ref[1] += n1;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                x[2 * h] -= n0;
+                x[2 * h + 1] -= n1;
+            }
             float vu = 1.f;
             if (sm > v_most) {   // (scales are bf16: below 2^128; an infinite one makes the output NaN)
                 const int e = static_cast<int>((__float_as_uint(sm) >> 23) & 0xff) - 127;   // sm < 2^(e + 1)
@@ -372,23 +403,19 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
             l_run[0] *= a0;
             l_run[1] *= a1;
         }
-        const float mu0 = m_ref[0] == kNegInf ? 0.f : m_ref[0], mu1 = m_ref[1] == kNegInf ? 0.f : m_ref[1];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {   // x becomes p
-            x[2 * h] = exp2_approx(x[2 * h] - mu0);
-            x[2 * h + 1] = exp2_approx(x[2 * h + 1] - mu1);
-        }
+        for (int e = 0; e < 8; ++e) x[e] = exp2_approx(x[e]);   // x becomes p
         l_run[0] += (x[0] + x[2]) + (x[4] + x[6]);
         l_run[1] += (x[1] + x[3]) + (x[5] + x[7]);
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch) {
-            uint32_t pb[4];   // P^T as the B operand, tokens 8 h ..
+            uint32_t pb[2][2];   // P^T as the B operand, tokens 16 g + 8 e ..
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
                 zo[ch][0] = fmaf(x[2 * h], vz[h][ch], zo[ch][0]);
                 zo[ch][1] = fmaf(x[2 * h + 1], vz[h][ch], zo[ch][1]);
                 const float sv = vs[h][ch] * v_unit;
-                pb[h] = movmatrix_trans(Mma<__half>::pack(x[2 * h] * sv, x[2 * h + 1] * sv));
+                pb[h / 2][h % 2] = movmatrix_trans(Mma<__half>::pack(x[2 * h] * sv, x[2 * h + 1] * sv));
             }
             uint32_t wa[4], wb[4];
             words(vbase, 0, ch, wa);
@@ -396,24 +423,18 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 const uint32_t a = wa[m], a8 = a >> 8, b = wb[m], b8 = b >> 8;
-                Mma<__half>::k16(o[4 * ch + m], a & 0x000f000fu, a & 0x00f000f0u, a8 & 0x000f000fu, a8 & 0x00f000f0u,
-                                 pb[0], pb[1]);
-                Mma<__half>::k16(o[4 * ch + m], b & 0x000f000fu, b & 0x00f000f0u, b8 & 0x000f000fu, b8 & 0x00f000f0u,
-                                 pb[2], pb[3]);
+                float(&y)[4] = o[4 * ch + m];
+                mma_f16(y, a & 0x000f000fu, a & 0x00f000f0u, a8 & 0x000f000fu, a8 & 0x00f000f0u, pb[0], y[0], y[1], y[2], y[3]);
+                mma_f16(y, b & 0x000f000fu, b & 0x00f000f0u, b8 & 0x000f000fu, b8 & 0x00f000f0u, pb[1], y[0], y[1], y[2], y[3]);
             }
         }
         __syncwarp();   // every lane has read the stage
-        if (i + ST < n_w) {
-            issue(i + ST);
-            ++issued;
-        }
+        if (i + ST < n_w) issue(i + ST, stage);
+        copy_group_end();
+        stage = stage == (ST - 1) * Sm::kStage ? 0u : stage + Sm::kStage;
     }
-    if (failed) {
-        if (lane == 0) flag_error(8 /* PA_DEVERR_TIMEOUT */);
-        // let the copies already in flight land before the CTA may exit
-        for (int k = i; k < issued; ++k) mbar_wait_bounded(&bars[k % ST], (k / ST) & 1, wait_limit_ns());
-    }
-    const int any_failed = __syncthreads_or(failed ? 1 : 0);   // (the ring is free now)
+    copy_groups_wait<0>();
+    __syncthreads();   // (the ring is free now)
 
     // ---- this warp's state in true units, then the warps' merge
     float* mo = reinterpret_cast<float*>(smem);
@@ -436,11 +457,8 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
                 row[16 * mt + 8 + r] = fmaf(o[mt][2 + e], back * 0.0625f, zo[mt / 4][e]);
             }
             if (r == 0) {
-                // a warp whose copies timed out counts as one without tokens: the
-                // call's outputs are not the attention then, but no merge reads
-                // what an earlier call left in the workspace
-                mml[(warp * kMaxGroup + h) * 2] = any_failed ? kNegInf : m_ref[e];
-                mml[(warp * kMaxGroup + h) * 2 + 1] = any_failed ? 0.f : l_run[e];
+                mml[(warp * kMaxGroup + h) * 2] = started ? m_ref[e] : kNegInf;
+                mml[(warp * kMaxGroup + h) * 2 + 1] = l_run[e];
             }
         }
     }

@@ -124,24 +124,36 @@ __device__ __forceinline__ void bulk_copy_g2s(void* dst, const void* src, uint32
         : "memory");
 }
 
+// Global -> shared copy of 16 bytes by this thread (both addresses 16-byte
+// aligned), past L1; complete once the thread has waited for its group.
+// (OFF: added to both, an immediate of the instruction)
+template <int OFF>
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0 + %3], [%1 + %3], 16, %2;" ::"r"(dst), "l"(src),
+                 "l"(policy), "n"(OFF)
+                 : "memory");
+}
+// `bytes` (a multiple of 512, or at most 512) by a warp whose lanes' addresses lie 16 bytes apart.
+template <int BYTES>
+__device__ __forceinline__ void copy_codes(uint32_t dst, const void* src, uint64_t policy) {
+    copy16_async<0>(dst, src, policy);
+    if constexpr (BYTES > 512) copy16_async<512>(dst, src, policy);
+    if constexpr (BYTES > 1024) copy16_async<1024>(dst, src, policy);
+    if constexpr (BYTES > 1536) copy16_async<1536>(dst, src, policy);
+    static_assert(BYTES <= 2048, "four copies at most");
+}
+__device__ __forceinline__ void copy_group_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of this thread's latest groups are still copying.
+template <int N>
+__device__ __forceinline__ void copy_groups_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Plain shared-memory loads (volatile: they must stay after the mbarrier
 // wait that makes the staged bytes visible).
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
-                 : "memory");
     return v;
 }
 __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
