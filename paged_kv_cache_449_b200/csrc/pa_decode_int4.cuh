@@ -10,13 +10,21 @@
 // accumulate; tokens or head dims as M, the heads of a GQA group as N) and
 // the scales and zeros cost a few fp32 operations a token and head.
 //
-// A code becomes an fp16 operand with one AND: four bits placed at the bottom
-// of an fp16 pattern are the subnormal code * 2^-24, four bits one nibble
-// higher code * 2^-20; the tensor cores multiply subnormals exactly.  The
-// factor 16 between the two is taken back where it is free: for K (nibble =
-// upper half of a 16-dim step) in the query operand, for V (nibble = upper
-// eight dims of a 16-dim tile) in the output rows.  A word of a tile is then a
-// whole operand of one MMA in five operations.
+// A byte holds the codes a and b of two dims (d and d + 8).  Put at the bottom
+// of an fp16 pattern it is the subnormal (a + 16 b) 2^-24, and its low four
+// bits are a 2^-24; the tensor cores multiply subnormals exactly.  So two ANDs
+// (or a byte permute and an AND) make the operands a and a + 16 b of both
+// bytes of a register, and the mixture is taken apart where that is free: for K,
+// whose two dims lie along the product's sum, in the query,
+//     a q_d + b q_d+8 = a (q_d - q_d+8 / 16) + (a + 16 b) (q_d+8 / 16),
+// for V, whose two dims are rows of the output, by one subtraction at the end.
+// A word of a tile is a whole operand of one MMA in four operations.
+//
+// Codes are taken about their middle, value = (zero + 7.5 scale) + scale (code
+// - 7.5): over many tokens of like weight sum p scale code and sum p zero
+// cancel, while the tensor core's sums lose up to 2^-24 of their size at every
+// product, always downwards (an error that grew with the square of the
+// tokens).  7.5 sum P comes from one more product, with ones, each 16 tokens.
 //
 // Each warp takes steps of 32 tokens (one online-softmax step each) from a
 // ring of shared-memory stages of its own, filled by asynchronous 16-byte
@@ -38,24 +46,21 @@
 namespace pa {
 
 // Query group for the fp16 product: rows scaled by 2^shift so that the largest
-// magnitude lands in [2^13, 2^14) (exact for every element within 2^-23 of it),
-// the upper eight dims of each 16-dim step by a further 1/16.  sums[c][e]: the
+// magnitude lands in [2^13, 2^14), the operands of a 16-dim step being q_d -
+// q_d+8 / 16 and q_d+8 / 16 (rounded to fp16, 2^-12 relative: at scores of
+// standard size 1e-4 of a unit, below what rounding P costs).  sums[c][e]: the
 // fp32 sum of dims 64 c .. of heads 2 (lane % 4) + e, unscaled.
+// `raw`: row r's dims 16 ks + 2c, + 1 and + 8 of them, as loaded (zero from row `group` on).
 template <typename T, int D>
-__device__ __forceinline__ int load_q_int4(uint32_t (&qa)[D / 16][2], float (&sums)[D / 64][2], const T* q_rows,
-                                           int group, int lane) {
-    const int r = lane >> 2, c = lane & 3;
+__device__ __forceinline__ int q_operands(uint32_t (&qa)[D / 16][2], float (&sums)[D / 64][2],
+                                          const uint32_t (&raw)[D / 16][2], int lane) {
+    const int c = lane & 3;
     float f[D / 16][4];
     float mx = 0.f;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t lo = 0u, hi = 0u;
-        if (r < group) {
-            lo = *reinterpret_cast<const uint32_t*>(q_rows + r * D + ks * 16 + 2 * c);
-            hi = *reinterpret_cast<const uint32_t*>(q_rows + r * D + ks * 16 + 8 + 2 * c);
-        }
-        const T* l = reinterpret_cast<const T*>(&lo);
-        const T* h = reinterpret_cast<const T*>(&hi);
+        const T* l = reinterpret_cast<const T*>(&raw[ks][0]);
+        const T* h = reinterpret_cast<const T*>(&raw[ks][1]);
         f[ks][0] = to_float<T>(l[0]);
         f[ks][1] = to_float<T>(l[1]);
         f[ks][2] = to_float<T>(h[0]);
@@ -77,8 +82,10 @@ __device__ __forceinline__ int load_q_int4(uint32_t (&qa)[D / 16][2], float (&su
         for (int m = 0; m < 4; ++m) {
             const float(&x)[4] = f[4 * ch + m];
             sum += (x[0] + x[1]) + (x[2] + x[3]);
-            const __half2 a = __floats2half2_rn(x[0] * mul, x[1] * mul);
-            const __half2 b = __floats2half2_rn(x[2] * mul * 0.0625f, x[3] * mul * 0.0625f);
+            // the operand pairs are (code, code + 16 code of the dim 8 on): see the kernel
+            const float b0 = x[2] * mul * 0.0625f, b1 = x[3] * mul * 0.0625f;
+            const __half2 a = __floats2half2_rn(x[0] * mul - b0, x[1] * mul - b1);
+            const __half2 b = __floats2half2_rn(b0, b1);
             qa[4 * ch + m][0] = *reinterpret_cast<const uint32_t*>(&a);
             qa[4 * ch + m][1] = *reinterpret_cast<const uint32_t*>(&b);
         }
@@ -120,6 +127,9 @@ struct VisibleSteps {
     __device__ __forceinline__ bool any(int t, int n) const { return t < L && (wlo - t < n || t < sinks); }
 };
 
+#ifndef PA_INT4_RESIDENT
+#define PA_INT4_RESIDENT 16   // warps an SM holds
+#endif
 template <int D, int B, int NW, int ST>
 struct Int4Smem {
     static constexpr int kTile = int4_tile_bytes(B, D);
@@ -132,8 +142,86 @@ struct Int4Smem {
     static_assert(kTile % 16 == 0, "copies move 16-byte units");
 };
 
+// Four output values x * inv, rounded once.
+template <typename T>
+__device__ __forceinline__ void store4(T* dst, const float4& x, float inv) {
+    uint2 w;
+    T* e = reinterpret_cast<T*>(&w);
+    e[0] = from_float<T>(x.x * inv);
+    e[1] = from_float<T>(x.y * inv);
+    e[2] = from_float<T>(x.z * inv);
+    e[3] = from_float<T>(x.w * inv);
+    *reinterpret_cast<uint2*>(dst) = w;
+}
+
+// The log-sum-exp merge of the np partials of (sequence, kv head) by one CTA:
+// first every partial's weight (a warp per head, lanes over partials, into
+// `weights`), then the weighted sums, eight partials' loads in flight a
+// thread.  The partials were written by other CTAs: read past L1.  More than
+// `room` weights go by merge_partitions_cta, one partial after the other.
+template <typename T, int D, int THREADS>
+__device__ __forceinline__ void merge_partials(const DecodeParams& p, int s, int kvh, int np, float* weights, int room) {
+    const int group = p.group;
+    if (static_cast<long long>(group) * np > room) {
+        merge_partitions_cta<T, D, true, THREADS>(p, s, kvh, np);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long row0 = static_cast<long long>(s) * p.num_q_heads + kvh * group;
+    for (int h = warp; h < group; h += THREADS / 32) {
+        const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + (row0 + h) * p.num_partitions;
+        float M = kNegInf;
+        for (int q = lane; q < np; q += 32) {
+            const float m = __ldcg(ml + q).x;
+            weights[h * np + q] = m;
+            M = fmaxf(M, m);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        const float top = M == kNegInf ? 0.f : M;
+        float den = 0.f;
+        for (int q = lane; q < np; q += 32) {
+            const float w = exp2_approx(weights[h * np + q] - top);
+            weights[h * np + q] = w;
+            den = fmaf(w, __ldcg(ml + q).y, den);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
+        const float inv = den > 0.f ? 1.f / den : 0.f;
+        for (int q = lane; q < np; q += 32) weights[h * np + q] *= inv;
+    }
+    __syncthreads();
+    for (int v = threadIdx.x; v < group * (D / 4); v += THREADS) {
+        const int h = v / (D / 4), c = v % (D / 4);
+        const float4* acc = reinterpret_cast<const float4*>(p.part_acc + (row0 + h) * p.num_partitions * D) + c;
+        const float* w = weights + h * np;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        int q = 0;
+        for (; q + 8 <= np; q += 8) {
+            float4 x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = __ldcg(acc + static_cast<long long>(q + k) * (D / 4));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                a.x = fmaf(w[q + k], x[k].x, a.x);
+                a.y = fmaf(w[q + k], x[k].y, a.y);
+                a.z = fmaf(w[q + k], x[k].z, a.z);
+                a.w = fmaf(w[q + k], x[k].w, a.w);
+            }
+        }
+        for (; q < np; ++q) {
+            const float4 x = __ldcg(acc + static_cast<long long>(q) * (D / 4));
+            a.x = fmaf(w[q], x.x, a.x);
+            a.y = fmaf(w[q], x.y, a.y);
+            a.z = fmaf(w[q], x.z, a.z);
+            a.w = fmaf(w[q], x.w, a.w);
+        }
+        store4<T>(reinterpret_cast<T*>(p.out) + (row0 + h) * D + 4 * c, a, 1.f);
+    }
+}
+
 template <typename T, int D, int B, int NW, int ST>
-__global__ void __launch_bounds__(NW * 32, 16 / NW)
+__global__ void __launch_bounds__(NW * 32, PA_INT4_RESIDENT / NW)
     pa_decode_int4_kernel(const __grid_constant__ DecodeParams p) {
     using Sm = Int4Smem<D, B, NW, ST>;
     constexpr int NC = D / 64;                   // groups of a row
@@ -156,6 +244,26 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
     }
     const int group = p.group;
     int L = p.context_lens[s];
+    // Asked for before the length is there: the query, and (without a window,
+    // where their places do not depend on it) the first block ids, of which
+    // those past the context are dropped below.
+    const int32_t* table = p.block_tables + static_cast<long long>(s) * p.max_blocks_per_seq;
+    auto early_ids = [&](int span) -> int {
+        const long long j = (static_cast<long long>(part) * p.partition_blocks + warp + (span * kSpan + lane / NB) * NW) * NB +
+                            lane % NB;
+        return p.window == 0 && j < p.max_blocks_per_seq ? __ldg(table + j) : -1;
+    };
+    const int early0 = early_ids(0), early1 = early_ids(1);
+    uint32_t qraw[D / 16][2];
+    {
+        const T* row = reinterpret_cast<const T*>(p.q) +
+                       (static_cast<long long>(s) * p.num_q_heads + kvh * group + r) * D + 2 * c;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            qraw[ks][0] = r < group ? *reinterpret_cast<const uint32_t*>(row + 16 * ks) : 0u;
+            qraw[ks][1] = r < group ? *reinterpret_cast<const uint32_t*>(row + 16 * ks + 8) : 0u;
+        }
+    }
     if (L < 0 || L > p.context_cap) {
         if (threadIdx.x == 0 && part == 0 && kvh == 0) flag_error(2 /* PA_DEVERR_CONTEXT_LEN */);
         L = L < 0 ? 0 : p.context_cap;
@@ -173,16 +281,15 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
     auto first_token = [&](int i) -> int { return 32 * vis.step(u0 + warp + i * NW); };
 
     // Block ids, kSpan steps at a time: lane = (step % kSpan) * NB + block of the step
-    const int32_t* table = p.block_tables + static_cast<long long>(s) * p.max_blocks_per_seq;
     bool refused = false;   // whether any id so far was (the whole warp knows)
-    auto load_ids = [&](int span) -> int {
+    auto load_ids = [&](int span, int early) -> int {
         const int i = span * kSpan + lane / NB;
         int id = -1;
         bool bad = false;
         if (i < n_w) {
             const int t = first_token(i) + lane % NB * B;
             if (vis.any(t, B)) {
-                id = __ldg(table + t / B);
+                id = span < 2 && p.window == 0 ? early : __ldg(table + t / B);
                 bad = id < 0 || static_cast<long long>(id) >= p.num_blocks;
                 if (bad) {
                     flag_error(1 /* PA_DEVERR_BLOCK_ID */);
@@ -193,7 +300,7 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
         refused = refused || __any_sync(0xffffffffu, bad);
         return id;
     };
-    int ids0 = load_ids(0), ids1 = load_ids(1);
+    int ids0 = load_ids(0, early0), ids1 = load_ids(1, early1);
     int span = 0;   // of ids0
 
     // Copies of step i (of the spans held) into its stage: for each tile the
@@ -232,8 +339,7 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
 
     uint32_t qa[D / 16][2];
     float qsum[NC][2];
-    const T* qrows = reinterpret_cast<const T*>(p.q) + (static_cast<long long>(s) * p.num_q_heads + kvh * group) * D;
-    const int shift = load_q_int4<T, D>(qa, qsum, qrows, group, lane);
+    const int shift = q_operands<T, D>(qa, qsum, qraw, lane);
     const float code_scale = ldexpf(p.score_scale, 24 - shift);
 #pragma unroll
     for (int ch = 0; ch < NC; ++ch) {
@@ -241,8 +347,9 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
         qsum[ch][1] *= p.score_scale;
     }
 
-    float o[D / 16][4];      // O^T of codes: (d = 16 mt + r, h = 2c), (d, 2c + 1), (d + 8, 2c) x 16, (d + 8, 2c + 1) x 16
-    float zo[NC][2];         // sum of p * zero, this lane's tokens
+    // O^T of codes less 7.5: (d = 16 mt + r, h = 2c), (d, 2c + 1), and that of d plus 16 times that of d + 8, the same heads
+    float o[D / 16][4];
+    float zo[NC][2];         // sum of p * (zero + 7.5 scale), this lane's tokens
     float m_ref[2] = {0.f, 0.f}, l_run[2] = {0.f, 0.f};
     bool started = false;    // whether a token has been attended: m_ref is a score then
     float v_unit = 0.f;      // scales of V are multiplied by this power of two (0: none seen yet)
@@ -287,7 +394,7 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
         if (i / kSpan != span) {
             ++span;
             ids0 = ids1;
-            ids1 = load_ids(span + 1);
+            ids1 = load_ids(span + 1, -1);
         }
         copy_groups_wait<ST - 1>();   // this lane's copies of the step; then every lane's
         __syncwarp();
@@ -312,14 +419,15 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
             words(kbase, 1, ch, wb);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const uint32_t a = wa[m], a8 = a >> 8, b = wb[m], b8 = b >> 8;
-                float(&x0)[4] = sc[0][ch];
-                float(&x1)[4] = sc[1][ch];
                 const bool first = m == 0;
-                mma_f16(x0, a & 0x000f000fu, a8 & 0x000f000fu, a & 0x00f000f0u, a8 & 0x00f000f0u, qa[4 * ch + m],
-                        first ? 0.f : x0[0], first ? 0.f : x0[1], first ? 0.f : x0[2], first ? 0.f : x0[3]);
-                mma_f16(x1, b & 0x000f000fu, b8 & 0x000f000fu, b & 0x00f000f0u, b8 & 0x00f000f0u, qa[4 * ch + m],
-                        first ? 0.f : x1[0], first ? 0.f : x1[1], first ? 0.f : x1[2], first ? 0.f : x1[3]);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {   // tokens r: bytes 0 and 2; r + 8: bytes 1 and 3
+                    const uint32_t w = g ? wb[m] : wa[m];
+                    const uint32_t e = w & 0x00ff00ffu, f = __byte_perm(w, 0u, 0x4341);
+                    float(&y)[4] = sc[g][ch];
+                    mma_f16(y, e & 0x000f000fu, f & 0x000f000fu, e, f, qa[4 * ch + m],
+                            first ? 0.f : y[0], first ? 0.f : y[1], first ? 0.f : y[2], first ? 0.f : y[3]);
+                }
             }
         }
         float vs[4][NC], vz[4][NC];
@@ -336,7 +444,7 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
                 x[2 * h] = fmaf(ks, q[2 * (h & 1)], fmaf(kz, qsum[ch][0], x[2 * h]));
                 x[2 * h + 1] = fmaf(ks, q[2 * (h & 1) + 1], fmaf(kz, qsum[ch][1], x[2 * h + 1]));
                 vs[h][ch] = __uint_as_float(vw[ch] << 16);
-                vz[h][ch] = __uint_as_float(vw[ch] & 0xffff0000u);
+                vz[h][ch] = fmaf(7.5f, vs[h][ch], __uint_as_float(vw[ch] & 0xffff0000u));   // the value of code 7.5
             }
         }
         if (!whole) {   // tokens that are not attended, or whose block id was refused: whatever lies there is not used
@@ -420,12 +528,23 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
             uint32_t wa[4], wb[4];
             words(vbase, 0, ch, wa);
             words(vbase, 1, ch, wb);
+            // the codes' mean part: 7.5 sum of P (as rounded), the same in every row
+            float mean[4];
+            mma_f16(mean, 0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u, pb[0], 0.f, 0.f, 0.f, 0.f);
+            mma_f16(mean, 0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u, pb[1], mean[0], mean[1], mean[2], mean[3]);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const uint32_t a = wa[m], a8 = a >> 8, b = wb[m], b8 = b >> 8;
                 float(&y)[4] = o[4 * ch + m];
-                mma_f16(y, a & 0x000f000fu, a & 0x00f000f0u, a8 & 0x000f000fu, a8 & 0x00f000f0u, pb[0], y[0], y[1], y[2], y[3]);
-                mma_f16(y, b & 0x000f000fu, b & 0x00f000f0u, b8 & 0x000f000fu, b8 & 0x00f000f0u, pb[1], y[0], y[1], y[2], y[3]);
+                y[0] = fmaf(-7.5f, mean[0], y[0]);
+                y[1] = fmaf(-7.5f, mean[1], y[1]);
+                y[2] = fmaf(-127.5f, mean[0], y[2]);
+                y[3] = fmaf(-127.5f, mean[1], y[3]);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {   // tokens 2c, 2c + 1: bytes 0 and 2; + 8: bytes 1 and 3
+                    const uint32_t w = g ? wb[m] : wa[m];
+                    const uint32_t e = w & 0x00ff00ffu, f = __byte_perm(w, 0u, 0x4341);
+                    mma_f16(y, e & 0x000f000fu, e, f & 0x000f000fu, f, pb[g], y[0], y[1], y[2], y[3]);
+                }
             }
         }
         __syncwarp();   // every lane has read the stage
@@ -454,7 +573,7 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt) {
                 row[16 * mt + r] = fmaf(o[mt][e], back, zo[mt / 4][e]);
-                row[16 * mt + 8 + r] = fmaf(o[mt][2 + e], back * 0.0625f, zo[mt / 4][e]);
+                row[16 * mt + 8 + r] = fmaf(o[mt][2 + e] - o[mt][e], back * 0.0625f, zo[mt / 4][e]);
             }
             if (r == 0) {
                 mml[(warp * kMaxGroup + h) * 2] = started ? m_ref[e] : kNegInf;
@@ -464,29 +583,30 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
     }
     __syncthreads();
     const int num_parts = (vis.n + p.partition_blocks - 1) / p.partition_blocks;
-    for (int idx = threadIdx.x; idx < group * D; idx += NW * 32) {
-        const int h = idx / D, d = idx - h * D;
-        float M = kNegInf;
+    for (int v = threadIdx.x; v < group * (D / 4); v += NW * 32) {   // four dims of a head each
+        const int h = v / (D / 4), d = v % (D / 4) * 4;
+        float m[NW], M = kNegInf;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, mml[(w * kMaxGroup + h) * 2]);
-        float num = 0.f, den = 0.f;
-        if (M != kNegInf) {
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, m[w] = mml[(w * kMaxGroup + h) * 2]);
+        const float top = M == kNegInf ? 0.f : M;
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+        float den = 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const float wt = exp2_approx(mml[(w * kMaxGroup + h) * 2] - M);
-                num = fmaf(wt, mo[(w * kMaxGroup + h) * kMergeRow<D> + d], num);
-                den = fmaf(wt, mml[(w * kMaxGroup + h) * 2 + 1], den);
-            }
+        for (int w = 0; w < NW; ++w) {
+            const float wt = exp2_approx(m[w] - top);
+            const float4 x = *reinterpret_cast<const float4*>(mo + (w * kMaxGroup + h) * kMergeRow<D> + d);
+            num.x = fmaf(wt, x.x, num.x);
+            num.y = fmaf(wt, x.y, num.y);
+            num.z = fmaf(wt, x.z, num.z);
+            num.w = fmaf(wt, x.w, num.w);
+            den = fmaf(wt, mml[(w * kMaxGroup + h) * 2 + 1], den);
         }
         if (num_parts > 1) {
             const long long slot = (static_cast<long long>(s) * p.num_q_heads + kvh * group + h) * p.num_partitions + part;
-            p.part_acc[slot * D + d] = num;
-            if (d == 0) {
-                p.part_ml[slot * 2] = M;
-                p.part_ml[slot * 2 + 1] = den;
-            }
+            *reinterpret_cast<float4*>(p.part_acc + slot * D + d) = num;
+            if (d == 0) *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(M, den);
         } else {
-            out[idx] = from_float<T>(den > 0.f ? num / den : 0.f);
+            store4<T>(out + h * D + d, num, den > 0.f ? 1.f / den : 0.f);
         }
     }
     if (num_parts > 1) {   // the CTA that brings a (sequence, kv head)'s last partition merges them
@@ -497,7 +617,7 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW)
         __syncthreads();
         if (last_arrival) {
             __threadfence();
-            merge_partitions_cta<T, D, true, NW * 32>(p, s, kvh, num_parts);
+            merge_partials<T, D, NW * 32>(p, s, kvh, num_parts, reinterpret_cast<float*>(smem), Sm::kArea / 4);
             if (threadIdx.x == 0) p.counters[static_cast<long long>(s) * p.num_kv_heads + kvh] = 0;
         }
     }
