@@ -985,19 +985,19 @@ long long window_partitions(long long units, int unit, int partition_size) {
     return (units + per - 1) / per;
 }
 
-// A partition size that gives the device's SMs about `ctas_per_sm` thread
-// blocks each: one pass where the sequences alone do, and no partition of
-// fewer than `least` tokens (a partition's start and merge cost about as much
-// as that many tokens' stream).
-int choose_partition(long long seqs, int num_kv_heads, long long units, int unit, int ctas_per_sm, int least) {
-    const long long pairs = seqs * num_kv_heads;
-    const long long want = static_cast<long long>(ctas_per_sm) * std::max(1, sm_count());
-    if (pairs <= 0 || units <= 0 || pairs >= want) return 0;
-    const long long parts = (want + pairs - 1) / pairs;
+// A partition size for units of `unit` tokens visible to each (sequence, kv
+// head): the work over the SMs once, between `least` and `enough` tokens (a
+// partition costs its thread block's start and its merge, so a batch that
+// fills the device takes no smaller ones), and more where that would be over
+// 16 partitions an SM.  0: one pass.
+int choose_partition(long long seqs, int num_kv_heads, long long units, int unit, int least, int enough) {
+    const long long tokens = units * unit, pairs = seqs * num_kv_heads, sms = std::max(1, sm_count());
+    if (pairs <= 0 || units <= 0) return 0;
+    const long long work = tokens > LLONG_MAX / pairs ? LLONG_MAX : tokens * pairs;
+    long long size = std::max(work / (16 * sms), std::min<long long>(std::max<long long>(work / sms, least), enough));
     const long long step = std::max(16, unit);   // partition sizes: multiples of both 16 and the block
-    long long size = (units * unit + parts - 1) / parts;
-    size = std::max<long long>((size + step - 1) / step * step, least);
-    return size >= units * unit || size > INT_MAX / 2 ? 0 : static_cast<int>(size);
+    size = (size + step - 1) / step * step;
+    return size >= tokens || size > INT_MAX / 2 ? 0 : static_cast<int>(size);
 }
 
 pa_status check_window(int window, int num_sinks, int least) {
@@ -1260,7 +1260,7 @@ pa_status pa_decode_int4_plan(int num_seqs, int num_q_heads, int num_kv_heads, i
         max_context_len < 0 || *partition_size < -1 || check_window(window, num_sinks, 0) != PA_OK)
         return PA_ERR_INVALID_ARG;
     const long long units = visible_units(max_context_len, window, num_sinks, kInt4Step);
-    if (*partition_size < 0) *partition_size = choose_partition(num_seqs, num_kv_heads, units, kInt4Step, 8, 256);
+    if (*partition_size < 0) *partition_size = choose_partition(num_seqs, num_kv_heads, units, kInt4Step, 128, 1024);
     if (*partition_size % kInt4Step != 0) return PA_ERR_INVALID_ARG;
     const long long parts = window_partitions(units, kInt4Step, *partition_size);
     *bytes = parts > 1 ? splitk_bytes(num_seqs, num_q_heads, parts, head_dim) : 0;
@@ -1318,7 +1318,7 @@ pa_status pa_decode_window_plan(int num_seqs, int num_q_heads, int num_kv_heads,
         return PA_ERR_INVALID_ARG;
     const long long units = visible_units(max_context_len, window, num_sinks, block_size);
     if (*partition_size < 0)
-        *partition_size = choose_partition(num_seqs, num_kv_heads, units, block_size, 4, 256);
+        *partition_size = choose_partition(num_seqs, num_kv_heads, units, block_size, 128, 1024);
     if (*partition_size % 16 != 0 || *partition_size % block_size != 0) return PA_ERR_INVALID_ARG;
     const long long parts = window_partitions(units, block_size, *partition_size);
     *bytes = parts > 1 ? splitk_bytes(num_seqs, num_q_heads, parts, head_dim) : 0;

@@ -24,7 +24,8 @@
 // - 7.5): over many tokens of like weight sum p scale code and sum p zero
 // cancel, while the tensor core's sums lose up to 2^-24 of their size at every
 // product, always downwards (an error that grew with the square of the
-// tokens).  7.5 sum P comes from one more product, with ones, each 16 tokens.
+// tokens).  7.5 sum P comes from one more product, with ones, each 16 tokens,
+// and leaves the accumulators every fourth step.
 //
 // Each warp takes steps of 32 tokens (one online-softmax step each) from a
 // ring of shared-memory stages of its own, filled by asynchronous 16-byte
@@ -127,9 +128,10 @@ struct VisibleSteps {
     __device__ __forceinline__ bool any(int t, int n) const { return t < L && (wlo - t < n || t < sinks); }
 };
 
-#ifndef PA_INT4_RESIDENT
-#define PA_INT4_RESIDENT 16   // warps an SM holds
-#endif
+// Warps an SM holds.  D = 128: 12 of 157 registers (one pass over 64 sequences
+// 30.6 us, the 70B long batch 142 us) rather than 16 of 128 (32.7 and 150 us).
+template <int D>
+constexpr int kInt4Resident = D == 128 ? 12 : 16;
 template <int D, int B, int NW, int ST>
 struct Int4Smem {
     static constexpr int kTile = int4_tile_bytes(B, D);
@@ -221,7 +223,7 @@ __device__ __forceinline__ void merge_partials(const DecodeParams& p, int s, int
 }
 
 template <typename T, int D, int B, int NW, int ST>
-__global__ void __launch_bounds__(NW * 32, PA_INT4_RESIDENT / NW)
+__global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
     pa_decode_int4_kernel(const __grid_constant__ DecodeParams p) {
     using Sm = Int4Smem<D, B, NW, ST>;
     constexpr int NC = D / 64;                   // groups of a row
@@ -349,6 +351,7 @@ __global__ void __launch_bounds__(NW * 32, PA_INT4_RESIDENT / NW)
 
     // O^T of codes less 7.5: (d = 16 mt + r, h = 2c), (d, 2c + 1), and that of d plus 16 times that of d + 8, the same heads
     float o[D / 16][4];
+    float ps[NC][2];         // sum of P (times 2^-24) that is still to come out of o
     float zo[NC][2];         // sum of p * (zero + 7.5 scale), this lane's tokens
     float m_ref[2] = {0.f, 0.f}, l_run[2] = {0.f, 0.f};
     bool started = false;    // whether a token has been attended: m_ref is a score then
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(NW * 32, PA_INT4_RESIDENT / NW)
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
 #pragma unroll
-    for (int ch = 0; ch < NC; ++ch) zo[ch][0] = zo[ch][1] = 0.f;
+    for (int ch = 0; ch < NC; ++ch) zo[ch][0] = zo[ch][1] = ps[ch][0] = ps[ch][1] = 0.f;
 
     // The four operand words of 16 tokens (half g of the step) and chunk ch,
     // and the group words of token 8 h + r, from the tiles at `base`.
@@ -389,6 +392,20 @@ __global__ void __launch_bounds__(NW * 32, PA_INT4_RESIDENT / NW)
         }
     };
 
+    auto centre = [&]() {   // takes 7.5 sum of P out of O
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                float(&y)[4] = o[4 * ch + m];
+                y[0] = fmaf(-7.5f, ps[ch][0], y[0]);
+                y[1] = fmaf(-7.5f, ps[ch][1], y[1]);
+                y[2] = fmaf(-127.5f, ps[ch][0], y[2]);
+                y[3] = fmaf(-127.5f, ps[ch][1], y[3]);
+            }
+            ps[ch][0] = ps[ch][1] = 0.f;
+        }
+    };
     uint32_t stage = 0;   // offset of step i's stage
     for (int i = 0; i < n_w; ++i) {
         if (i / kSpan != span) {
@@ -430,7 +447,7 @@ __global__ void __launch_bounds__(NW * 32, PA_INT4_RESIDENT / NW)
                 }
             }
         }
-        float vs[4][NC], vz[4][NC];
+        float vs[4][NC], vz[4][NC];   // V's scales, and the values of code 7.5
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             uint32_t kw[NC], vw[NC];
@@ -444,7 +461,7 @@ __global__ void __launch_bounds__(NW * 32, PA_INT4_RESIDENT / NW)
                 x[2 * h] = fmaf(ks, q[2 * (h & 1)], fmaf(kz, qsum[ch][0], x[2 * h]));
                 x[2 * h + 1] = fmaf(ks, q[2 * (h & 1) + 1], fmaf(kz, qsum[ch][1], x[2 * h + 1]));
                 vs[h][ch] = __uint_as_float(vw[ch] << 16);
-                vz[h][ch] = fmaf(7.5f, vs[h][ch], __uint_as_float(vw[ch] & 0xffff0000u));   // the value of code 7.5
+                vz[h][ch] = fmaf(7.5f, vs[h][ch], __uint_as_float(vw[ch] & 0xffff0000u));
             }
         }
         if (!whole) {   // tokens that are not attended, or whose block id was refused: whatever lies there is not used
@@ -507,6 +524,8 @@ __global__ void __launch_bounds__(NW * 32, PA_INT4_RESIDENT / NW)
             for (int ch = 0; ch < NC; ++ch) {
                 zo[ch][0] *= a0;
                 zo[ch][1] *= a1;
+                ps[ch][0] *= a0 * vu;
+                ps[ch][1] *= a1 * vu;
             }
             l_run[0] *= a0;
             l_run[1] *= a1;
@@ -530,15 +549,13 @@ __global__ void __launch_bounds__(NW * 32, PA_INT4_RESIDENT / NW)
             words(vbase, 1, ch, wb);
             // the codes' mean part: 7.5 sum of P (as rounded), the same in every row
             float mean[4];
-            mma_f16(mean, 0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u, pb[0], 0.f, 0.f, 0.f, 0.f);
+            mma_f16(mean, 0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u, pb[0], ps[ch][0], ps[ch][1], 0.f, 0.f);
             mma_f16(mean, 0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u, pb[1], mean[0], mean[1], mean[2], mean[3]);
+            ps[ch][0] = mean[0];
+            ps[ch][1] = mean[1];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 float(&y)[4] = o[4 * ch + m];
-                y[0] = fmaf(-7.5f, mean[0], y[0]);
-                y[1] = fmaf(-7.5f, mean[1], y[1]);
-                y[2] = fmaf(-127.5f, mean[0], y[2]);
-                y[3] = fmaf(-127.5f, mean[1], y[3]);
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {   // tokens 2c, 2c + 1: bytes 0 and 2; + 8: bytes 1 and 3
                     const uint32_t w = g ? wb[m] : wa[m];
@@ -547,11 +564,13 @@ __global__ void __launch_bounds__(NW * 32, PA_INT4_RESIDENT / NW)
                 }
             }
         }
+        if ((i & 3) == 3) centre();
         __syncwarp();   // every lane has read the stage
         if (i + ST < n_w) issue(i + ST, stage);
         copy_group_end();
         stage = stage == (ST - 1) * Sm::kStage ? 0u : stage + Sm::kStage;
     }
+    centre();
     copy_groups_wait<0>();
     __syncthreads();   // (the ring is free now)
 
@@ -610,10 +629,12 @@ __global__ void __launch_bounds__(NW * 32, PA_INT4_RESIDENT / NW)
         }
     }
     if (num_parts > 1) {   // the CTA that brings a (sequence, kv head)'s last partition merges them
-        __threadfence();
+        // (the barrier orders the CTA's writes before thread 0's fence, which covers them)
         __syncthreads();
-        if (threadIdx.x == 0)
+        if (threadIdx.x == 0) {
+            __threadfence();
             last_arrival = atomicAdd(p.counters + static_cast<long long>(s) * p.num_kv_heads + kvh, 1) == num_parts - 1;
+        }
         __syncthreads();
         if (last_arrival) {
             __threadfence();
