@@ -1088,6 +1088,9 @@ pa_status check_row_shape(int64_t num_tokens, int num_kv_heads, int head_dim, in
     return PA_OK;
 }
 
+#ifndef PA_INT4_FEW_ROWS
+#define PA_INT4_FEW_ROWS 2048
+#endif
 template <bool WRITE>
 pa_status rows_int4(void* key, void* value, void* k_cache, void* v_cache, const int64_t* slot_mapping,
                     int64_t num_tokens, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
@@ -1108,15 +1111,21 @@ pa_status rows_int4(void* key, void* value, void* k_cache, void* v_cache, const 
     p.block_size = block_size;
     p.num_slots = num_blocks * static_cast<long long>(block_size);
     if (num_tokens > LLONG_MAX / 4096 / num_kv_heads) return PA_ERR_UNSUPPORTED;
-    const long long threads = num_tokens * num_kv_heads * (head_dim * elem_size(dtype) / 16);
-    const long long blocks = (threads + 255) / 256;
+    // Few tokens go row by row, a thread for each 16-byte vector; many by
+    // groups of a block's tokens, a warp for each (PA_INT4_ROWS_TOKENS).
+    const bool rows = num_tokens * num_kv_heads <= PA_INT4_FEW_ROWS;
+    const int group = block_size == 8 ? 8 : 16;
+    const long long blocks = rows ? (num_tokens * num_kv_heads * (head_dim * elem_size(dtype) / 16) + 255) / 256
+                                  : ((num_tokens + group - 1) / group * num_kv_heads + 3) / 4;
     if (blocks > INT_MAX) return PA_ERR_UNSUPPORTED;
     const cudaError_t e = with_rows(dtype, head_dim, [&](auto tt, auto dd) -> cudaError_t {
         using T = typename decltype(tt)::type;
         constexpr int kD = decltype(dd)::value;
-        return launch_early(WRITE ? pa::pa_reshape_int4_kernel<T, kD> : pa::pa_gather_int4_kernel<T, kD>,
-                            dim3(static_cast<unsigned>(blocks)), dim3(256), 0, static_cast<cudaStream_t>(stream),
-                            PA_EARLY_LAUNCH, p);
+        auto kernel = rows ? pa::pa_rows_int4_kernel<T, kD, WRITE>
+                           : (group == 8 ? pa::pa_groups_int4_kernel<T, kD, 8, WRITE>
+                                         : pa::pa_groups_int4_kernel<T, kD, 16, WRITE>);
+        return launch_early(kernel, dim3(static_cast<unsigned>(blocks)), dim3(rows ? 256 : 128), 0,
+                            static_cast<cudaStream_t>(stream), PA_EARLY_LAUNCH, p);
     });
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

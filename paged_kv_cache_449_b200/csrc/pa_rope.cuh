@@ -44,103 +44,122 @@ struct RopeParams {
     long long num_slots;
 };
 
+#ifndef PA_ROPE_ROWS
+#define PA_ROPE_ROWS 3
+#endif
+#ifndef PA_ROPE_CTAS
+#define PA_ROPE_CTAS 4
+#endif
+constexpr int kRopeRows = PA_ROPE_ROWS;
 constexpr int kRopeThreads = 256;
 
-// One CTA per token; a group of D / E lanes takes one head's row at a time.
+// One CTA per token; a group of D / E lanes takes one head's row at a time,
+// kRopeRows rows in flight: their loads are asked for first, then the token's
+// sines and cosines computed while they come.
 template <typename T, int D, Pool POOL, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads) pa_rope_cache_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, PA_ROPE_CTAS) pa_rope_cache_kernel(const __grid_constant__ RopeParams p) {
     wait_for_prior_work();
     constexpr int E = Vec<T>::E, V = D / E;
-    __shared__ float2 turn[D / 2];   // m cos, m sin
+    constexpr int kStep = kRopeThreads / V;   // rows the CTA takes at once
+    __shared__ float2 turn[D / 2];            // m cos, m sin
     const long long i = blockIdx.x;
     const long long slot = p.slot_mapping[i];
+    const int vec = threadIdx.x % V, lane = threadIdx.x & 31;
+    const int rows = p.num_q_heads + 2 * p.num_kv_heads, v_row = p.num_q_heads + p.num_kv_heads;
     const int half = p.rotary_dim / 2;
+    const bool live = slot >= 0 && slot < p.num_slots;
+
+    uint4 raw[kRopeRows];
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int k = 0; k < kRopeRows; ++k) {
+            const int row = r0 + k * kStep;
+            const T* src = reinterpret_cast<const T*>(p.q) + i * p.q_stride + row * D;
+            if (row >= p.num_q_heads) src = reinterpret_cast<const T*>(p.key) + i * p.k_stride + (row - p.num_q_heads) * D;
+            if (row >= v_row) src = reinterpret_cast<const T*>(p.value) + i * p.v_stride + (row - v_row) * D;
+            raw[k] = row < rows ? *reinterpret_cast<const uint4*>(src + vec * E) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    const int first = threadIdx.x / V;
+    load(first);
     for (int j = threadIdx.x; j < half; j += kRopeThreads) {
-        const double turns = static_cast<double>(p.positions[i]) * (static_cast<double>(p.inv_freq[j]) * 0.15915494309189533577);
+        const double turns =
+            static_cast<double>(p.positions[i]) * (static_cast<double>(p.inv_freq[j]) * 0.15915494309189533577);
         const float part = static_cast<float>(turns - rint(turns));   // of a turn, [-1/2, 1/2]
         float s, c;
         sincospif(2.f * part, &s, &c);
         turn[j] = make_float2(c * p.rope_scale, s * p.rope_scale);
     }
-    __syncthreads();
     if (slot >= p.num_slots && threadIdx.x == 0) flag_error(4 /* PA_DEVERR_SLOT */);
-    const bool live = slot >= 0 && slot < p.num_slots;
     const long long block = live ? slot / p.block_size : 0;
     const int t = live ? static_cast<int>(slot - block * p.block_size) : 0;
-    const int vec = threadIdx.x % V;
-    const int rows = p.num_q_heads + 2 * p.num_kv_heads;
-    const int step = kRopeThreads / V;
-    const int first = threadIdx.x / V;
+    __syncthreads();
+
     // every lane of a warp takes the same number of turns: the shuffles stay whole
-    for (int r0 = 0; r0 < rows; r0 += step) {
-        const int row = r0 + first;
-        const bool in = row < rows;
-        const bool is_q = row < p.num_q_heads, is_v = row >= p.num_q_heads + p.num_kv_heads;
-        const int h = is_q ? row : (is_v ? row - p.num_q_heads - p.num_kv_heads : row - p.num_q_heads);
-        const T* src = reinterpret_cast<const T*>(is_q ? p.q : (is_v ? p.value : p.key)) +
-                       i * (is_q ? p.q_stride : (is_v ? p.v_stride : p.k_stride)) + h * D + vec * E;
-        Vec<T> x;
-        if (in) x.load(src);
-        else
+    for (int r0 = first; r0 - first < rows; r0 += kRopeRows * kStep) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) x.f[e] = 0.f;
-        const T* w = reinterpret_cast<const T*>(is_q ? p.q_weight : p.k_weight);
-        float sum = 0.f;
+        for (int k = 0; k < kRopeRows; ++k) {
+            const int row = r0 + k * kStep;
+            if (row - first >= rows) break;   // (uniform)
+            const bool in = row < rows, is_q = row < p.num_q_heads, is_v = row >= v_row;
+            const int h = is_q ? row : (is_v ? row - v_row : row - p.num_q_heads);
+            Vec<T> x;
+            x.widen(raw[k]);
+            const T* w = reinterpret_cast<const T*>(is_q ? p.q_weight : p.k_weight);
+            if (p.q_weight != nullptr || p.k_weight != nullptr) {
+                float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum = fmaf(x.f[e], x.f[e], sum);
+                for (int e = 0; e < E; ++e) sum = fmaf(x.f[e], x.f[e], sum);
 #pragma unroll
-        for (int off = 1; off < V; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (!is_v && w != nullptr) {
-            const float inv = 1.f / sqrtf(sum * (1.f / D) + p.eps);
-            Vec<T> g;
-            g.load(w + vec * E);
+                for (int off = 1; off < V; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                if (!is_v && w != nullptr) {
+                    const float inv = 1.f / sqrtf(sum * (1.f / D) + p.eps);
+                    Vec<T> g;
+                    g.load(w + vec * E);
 #pragma unroll
-            for (int e = 0; e < E; ++e) x.f[e] = x.f[e] * inv * g.f[e];
-        }
-        if constexpr (INTERLEAVED) {
-            if (!is_v) {
+                    for (int e = 0; e < E; ++e) x.f[e] = x.f[e] * inv * g.f[e];
+                }
+            }
+            if constexpr (INTERLEAVED) {
+                if (!is_v) {
 #pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const int d = vec * E + e;
-                    if (d < p.rotary_dim) {
-                        const float2 cs = turn[d / 2];
-                        const float a = x.f[e], b = x.f[e + 1];
-                        x.f[e] = a * cs.x - b * cs.y;
-                        x.f[e + 1] = b * cs.x + a * cs.y;
+                    for (int e = 0; e < E; e += 2) {
+                        const int d = vec * E + e;
+                        if (d < p.rotary_dim) {
+                            const float2 cs = turn[d / 2];
+                            const float a = x.f[e], b = x.f[e + 1];
+                            x.f[e] = a * cs.x - b * cs.y;
+                            x.f[e + 1] = b * cs.x + a * cs.y;
+                        }
+                    }
+                }
+            } else {
+                // the other element of each pair lies half / E lanes away
+                const int hop = half / E;
+                const bool low = vec < hop, turned = vec < 2 * hop;
+                const int from = turned ? lane + (low ? hop : -hop) : lane;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float y = __shfl_sync(0xffffffffu, x.f[e], from);
+                    if (turned && !is_v) {
+                        const float2 cs = turn[(low ? vec : vec - hop) * E + e];
+                        x.f[e] = low ? x.f[e] * cs.x - y * cs.y : x.f[e] * cs.x + y * cs.y;
                     }
                 }
             }
-        } else {
-            // the other element of each pair lies half / E lanes away
-            const int hop = half / E;
-            const bool low = vec < hop;
-            const int from = (threadIdx.x & 31) + (low ? hop : -hop);
-            const bool turned = vec < 2 * hop;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float y = __shfl_sync(0xffffffffu, x.f[e], turned ? from : (threadIdx.x & 31));
-                if (turned && !is_v) {
-                    const float2 cs = turn[(low ? vec : vec - hop) * E + e];
-                    x.f[e] = low ? x.f[e] * cs.x - y * cs.y : x.f[e] * cs.x + y * cs.y;
-                }
-            }
-        }
-        if (is_q) {
-            if (in)
+            if (is_q && in)
                 *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.q_out) + (i * p.num_q_heads + h) * D + vec * E) = x.narrow();
-        }
-        const bool write = in && !is_q && live;
-        float scale8 = 1.f;
-        if constexpr (POOL == Pool::kE4m3) scale8 = write ? (is_v ? p.v_scale : p.k_scale)[h] : 1.f;
-        if constexpr (POOL == Pool::kInt4) {   // (what the pool holds is the rounded row's code)
+            const bool write = in && !is_q && live;
+            float scale8 = 1.f;
+            if constexpr (POOL == Pool::kE4m3) scale8 = write ? (is_v ? p.v_scale : p.k_scale)[h] : 1.f;
+            if constexpr (POOL != Pool::kNative) {   // (what a quantised pool holds is the rounded row's code)
 #pragma unroll
-            for (int e = 0; e < E; ++e) x.f[e] = to_float<T>(from_float<T>(x.f[e]));
-        } else if constexpr (POOL == Pool::kE4m3) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) x.f[e] = to_float<T>(from_float<T>(x.f[e]));
+                for (int e = 0; e < E; ++e) x.f[e] = to_float<T>(from_float<T>(x.f[e]));
+            }
+            write_row<T, D, POOL>(x, is_v ? p.v_cache : p.k_cache, write ? block * p.num_kv_heads + h : 0,
+                                  p.block_size, t, vec, is_v, scale8, write, 0xffffffffu);
         }
-        write_row<T, D, POOL>(x, is_v ? p.v_cache : p.k_cache, write ? block * p.num_kv_heads + h : 0, p.block_size,
-                              t, vec, is_v, scale8, write, 0xffffffffu);
+        if (r0 - first + kRopeRows * kStep < rows) load(r0 + kRopeRows * kStep);
     }
 }
 

@@ -85,12 +85,76 @@ def test_write_and_read_back_bit_for_bit(B, D, dtype):
     assert pa.pa_get_device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D,B", [(64, 8), (64, 16), (128, 32), (128, 8), (128, 16)])
+def test_many_tokens_bit_for_bit(D, B, dtype):
+    """Chunks that start and end anywhere in their blocks, padding, single
+    tokens, a run of slots that crosses into another block's."""
+    g = ou.gen(D + B)
+    H, N = 7, 64
+    order = torch.randperm(N, generator=g)
+    slots, used = [], 0
+    for start, count in ((5, 150), (0, 97), (B - 1, 2 * B + 3), (3, 1), (0, B), (7, 100)):
+        blocks = order[used:used + (start + count + B - 1) // B]
+        used += len(blocks)
+        slots += [int(blocks[(start + i) // B]) * B + (start + i) % B for i in range(count)]
+        slots.append(-1)
+    free = [int(b) * B + t for b in order[used:used + 3] for t in torch.randperm(B, generator=g).tolist()]
+    slots = torch.tensor(slots + free)
+    T = len(slots)
+    assert T * H > 2048 and used + 3 <= N
+    k, v = ou.normal((T, H, D), dtype, g), ou.normal((T, H, D), dtype, g)
+    k[:, :, 0] = torch.arange(T)[:, None] / 4.0            # quotients that are ties, or near them
+    k[3], v[4] = 0.25, 0
+    v[:, 0] = torch.arange(D) % 64 / 8.0
+    v[6] *= 1e-30 if dtype != torch.float16 else 1e-7
+    kc, vc = empty_pools(N, H, D, B, 0xee)
+    got = [x.cuda() for x in (kc, vc)]
+    ops.pa_reshape_and_cache_int4(k.cuda(), v.cuda(), *got, slots.cuda())
+    for pool, rows, side in ((kc, k, False), (vc, v, True)):
+        ou.write4(pool, rows, slots, B, side)
+    for a, b in zip(got, (kc, vc)):
+        assert torch.equal(a.cpu(), b)
+    back = [torch.full_like(k, 7).cuda(), torch.full_like(v, 7).cuda()]
+    ops.pa_gather_cache_int4(*back, *got, slots.cuda())
+    for x, rows in zip(back, (k, v)):
+        want = ou.values4(rows).to(torch.float32).to(dtype)
+        want[slots < 0] = 7
+        assert torch.equal(x.cpu(), want)
+    assert pa.pa_get_device_error() == 0
+
+
+def test_a_row_that_is_not_finite_keeps_to_itself():
+    D, B, T, H = 128, 16, 1024, 3
+    g = ou.gen(4)
+    k, v = ou.normal((T, H, D), torch.bfloat16, g), ou.normal((T, H, D), torch.bfloat16, g)
+    slots = torch.arange(T)
+    pools = []
+    for bad in (False, True):
+        if bad:
+            k[5, 1, 3], k[17, 0, 70], v[5, 1, 3], v[30, 2, 9] = float("nan"), float("inf"), float("-inf"), float("nan")
+        kc, vc = (x.cuda() for x in empty_pools(T // B, H, D, B))
+        ops.pa_reshape_and_cache_int4(k.cuda(), v.cuda(), kc, vc, slots.cuda())
+        back = [torch.zeros_like(k).cuda(), torch.zeros_like(k).cuda()]
+        ops.pa_gather_cache_int4(*back, kc, vc, slots.cuda())
+        pools.append([x.cpu() for x in back])
+    for x, y in zip(*pools):
+        x, y = x.unflatten(2, (2, 64)), y.unflatten(2, (2, 64))
+        same = (x == y).all(-1)
+        assert (~same).sum() <= 2      # the groups that hold such a value
+
+
 @pytest.mark.parametrize("write", [True, False])
 def test_a_slot_past_the_pool_is_flagged(write):
     k = torch.ones(2, 1, 64, dtype=torch.float16).cuda()
     kc, vc = (x.cuda() for x in empty_pools(2, 1, 64, 8))
     fn = ops.pa_reshape_and_cache_int4 if write else ops.pa_gather_cache_int4
     fn(k, k.clone(), kc, vc, torch.tensor([16, 3]).cuda())
+    assert pa.pa_get_device_error() == pa.DEVERR_SLOT
+    many = torch.ones(3000, 1, 64, dtype=torch.float16).cuda()
+    slots = torch.full((3000,), -1, dtype=torch.int64)
+    slots[100:108] = torch.arange(12, 20)      # a run that leaves the pool
+    fn(many, many.clone(), kc, vc, slots.cuda())
     assert pa.pa_get_device_error() == pa.DEVERR_SLOT
 
 
