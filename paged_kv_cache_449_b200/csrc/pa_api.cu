@@ -1116,7 +1116,7 @@ pa_status rows_int4(void* key, void* value, void* k_cache, void* v_cache, const 
     const bool rows = num_tokens * num_kv_heads <= PA_INT4_FEW_ROWS;
     const int group = block_size == 8 ? 8 : 16;
     const long long blocks = rows ? (num_tokens * num_kv_heads * (head_dim * elem_size(dtype) / 16) + 255) / 256
-                                  : ((num_tokens + group - 1) / group * num_kv_heads + 3) / 4;
+                                  : ((num_tokens + group - 1) / group * num_kv_heads + 1) / 2;
     if (blocks > INT_MAX) return PA_ERR_UNSUPPORTED;
     const cudaError_t e = with_rows(dtype, head_dim, [&](auto tt, auto dd) -> cudaError_t {
         using T = typename decltype(tt)::type;
@@ -1187,8 +1187,12 @@ pa_status rope_and_cache(void* q_out, const void* q, const void* key, const void
     const cudaError_t e = with_rows(dtype, head_dim, [&](auto tt, auto dd) -> cudaError_t {
         using T = typename decltype(tt)::type;
         constexpr int kD = decltype(dd)::value;
-        return launch_early(interleaved ? pa::pa_rope_cache_kernel<T, kD, POOL, true>
-                                        : pa::pa_rope_cache_kernel<T, kD, POOL, false>,
+        const bool norm = q_weight != nullptr || k_weight != nullptr;
+        auto kernel = interleaved ? (norm ? pa::pa_rope_cache_kernel<T, kD, POOL, true, true>
+                                          : pa::pa_rope_cache_kernel<T, kD, POOL, true, false>)
+                                  : (norm ? pa::pa_rope_cache_kernel<T, kD, POOL, false, true>
+                                          : pa::pa_rope_cache_kernel<T, kD, POOL, false, false>);
+        return launch_early(kernel,
                             dim3(static_cast<unsigned>(num_tokens)), dim3(pa::kRopeThreads), 0,
                             static_cast<cudaStream_t>(stream), PA_EARLY_LAUNCH, p);
     });

@@ -56,8 +56,8 @@ constexpr int kRopeThreads = 256;
 // One CTA per token; a group of D / E lanes takes one head's row at a time,
 // kRopeRows rows in flight: their loads are asked for first, then the token's
 // sines and cosines computed while they come.
-template <typename T, int D, Pool POOL, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads, PA_ROPE_CTAS) pa_rope_cache_kernel(const __grid_constant__ RopeParams p) {
+template <typename T, int D, Pool POOL, bool INTERLEAVED, bool NORM>
+__global__ void __launch_bounds__(kRopeThreads, POOL == Pool::kNative ? PA_ROPE_CTAS : 3) pa_rope_cache_kernel(const __grid_constant__ RopeParams p) {
     wait_for_prior_work();
     constexpr int E = Vec<T>::E, V = D / E;
     constexpr int kStep = kRopeThreads / V;   // rows the CTA takes at once
@@ -94,6 +94,22 @@ __global__ void __launch_bounds__(kRopeThreads, PA_ROPE_CTAS) pa_rope_cache_kern
     const long long block = live ? slot / p.block_size : 0;
     const int t = live ? static_cast<int>(slot - block * p.block_size) : 0;
     __syncthreads();
+    // This thread's dims are the same in every row, and so are its angles.
+    // Half layout: x' = x cos + y sin', y the pair's other element, which lies
+    // half / E lanes away, sin' = -sin in the pair's first half.
+    const int hop = half / E;
+    const bool low = vec < hop, turned = INTERLEAVED ? vec * E < p.rotary_dim : vec < 2 * hop;
+    const int from = turned ? lane + (low ? hop : -hop) : lane;
+    constexpr int kPairs = INTERLEAVED ? E / 2 : E;
+    float cs[kPairs], sn[kPairs];
+    if (turned) {
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) {
+            const float2 a = turn[INTERLEAVED ? vec * (E / 2) + e : (low ? vec : vec - hop) * E + e];
+            cs[e] = a.x;
+            sn[e] = !INTERLEAVED && low ? -a.y : a.y;
+        }
+    }
 
     // every lane of a warp takes the same number of turns: the shuffles stay whole
     for (int r0 = first; r0 - first < rows; r0 += kRopeRows * kStep) {
@@ -103,10 +119,18 @@ __global__ void __launch_bounds__(kRopeThreads, PA_ROPE_CTAS) pa_rope_cache_kern
             if (row - first >= rows) break;   // (uniform)
             const bool in = row < rows, is_q = row < p.num_q_heads, is_v = row >= v_row;
             const int h = is_q ? row : (is_v ? row - v_row : row - p.num_q_heads);
+            const bool write = in && !is_q && live;
+            const long long tile = write ? block * p.num_kv_heads + h : 0;
+            if (POOL == Pool::kNative && __all_sync(0xffffffffu, is_v)) {   // a warp of V rows: copied as they are
+                if (write)
+                    *reinterpret_cast<uint4*>(p.v_cache + tile * p.block_size * D * static_cast<int>(sizeof(T)) +
+                                              (vec * p.block_size + t) * 16) = raw[k];
+                continue;
+            }
             Vec<T> x;
             x.widen(raw[k]);
-            const T* w = reinterpret_cast<const T*>(is_q ? p.q_weight : p.k_weight);
-            if (p.q_weight != nullptr || p.k_weight != nullptr) {
+            if constexpr (NORM) {
+                const T* w = reinterpret_cast<const T*>(is_q ? p.q_weight : p.k_weight);
                 float sum = 0.f;
 #pragma unroll
                 for (int e = 0; e < E; ++e) sum = fmaf(x.f[e], x.f[e], sum);
@@ -121,43 +145,32 @@ __global__ void __launch_bounds__(kRopeThreads, PA_ROPE_CTAS) pa_rope_cache_kern
                 }
             }
             if constexpr (INTERLEAVED) {
-                if (!is_v) {
+                if (turned && !is_v) {
 #pragma unroll
                     for (int e = 0; e < E; e += 2) {
-                        const int d = vec * E + e;
-                        if (d < p.rotary_dim) {
-                            const float2 cs = turn[d / 2];
-                            const float a = x.f[e], b = x.f[e + 1];
-                            x.f[e] = a * cs.x - b * cs.y;
-                            x.f[e + 1] = b * cs.x + a * cs.y;
-                        }
+                        const float a = x.f[e], b = x.f[e + 1];
+                        x.f[e] = a * cs[e / 2] - b * sn[e / 2];
+                        x.f[e + 1] = b * cs[e / 2] + a * sn[e / 2];
                     }
                 }
             } else {
-                // the other element of each pair lies half / E lanes away
-                const int hop = half / E;
-                const bool low = vec < hop, turned = vec < 2 * hop;
-                const int from = turned ? lane + (low ? hop : -hop) : lane;
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     const float y = __shfl_sync(0xffffffffu, x.f[e], from);
-                    if (turned && !is_v) {
-                        const float2 cs = turn[(low ? vec : vec - hop) * E + e];
-                        x.f[e] = low ? x.f[e] * cs.x - y * cs.y : x.f[e] * cs.x + y * cs.y;
-                    }
+                    if (turned && !is_v) x.f[e] = x.f[e] * cs[e] + y * sn[e];
                 }
             }
             if (is_q && in)
                 *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.q_out) + (i * p.num_q_heads + h) * D + vec * E) = x.narrow();
-            const bool write = in && !is_q && live;
+            if (__all_sync(0xffffffffu, is_q)) continue;
             float scale8 = 1.f;
             if constexpr (POOL == Pool::kE4m3) scale8 = write ? (is_v ? p.v_scale : p.k_scale)[h] : 1.f;
             if constexpr (POOL != Pool::kNative) {   // (what a quantised pool holds is the rounded row's code)
 #pragma unroll
                 for (int e = 0; e < E; ++e) x.f[e] = to_float<T>(from_float<T>(x.f[e]));
             }
-            write_row<T, D, POOL>(x, is_v ? p.v_cache : p.k_cache, write ? block * p.num_kv_heads + h : 0,
-                                  p.block_size, t, vec, is_v, scale8, write, 0xffffffffu);
+            write_row<T, D, POOL>(x, is_v ? p.v_cache : p.k_cache, tile, p.block_size, t, vec, is_v, scale8, write,
+                                  0xffffffffu);
         }
         if (r0 - first + kRopeRows * kStep < rows) load(r0 + kRopeRows * kStep);
     }

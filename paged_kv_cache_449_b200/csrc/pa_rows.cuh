@@ -9,9 +9,9 @@
 // scale and a zero:
 //     zero  = the group's minimum rounded down to bf16
 //     scale = (maximum - zero) / 15 rounded up to bf16 (0 if that is 0, else at least 2^-126)
-//     code  = (x - zero) / scale rounded to the nearest whole number, ties to even, in 0..15
+//     code  = (x - zero) / scale to the nearest whole number, ties to even, in 0..15
 //     value = zero + scale * code
-// (every step in fp32).  The roundings outwards keep the whole group inside
+// (in fp32, the quotient of the fp32 difference exact).  The roundings outwards keep the whole group inside
 // [zero, zero + 15 scale], so no value is clipped by more than fp32's own
 // rounding; bf16 covers every input type's range, where fp16 would not.
 // Groups of 64 dims cost 4 bytes per 32 bytes of codes.
@@ -69,23 +69,49 @@ struct Vec {
     }
 };
 
-// Scale and zero of the group whose smallest and largest element are mn, mx.
-__device__ __forceinline__ uint32_t int4_group_word(float mn, float mx, float& scale, float& zero) {
+// Scale, zero and 1 / scale of the group whose smallest and largest element
+// are mn, mx.  A group that is not finite keeps a zero that is not, and codes 0
+// (inv and scale 0 for them), so that its bytes concern no other row.
+__device__ __forceinline__ uint32_t int4_group_word(float mn, float mx, float& scale, float& inv, float& zero) {
     const __nv_bfloat16 z = __float2bfloat16_rd(mn + 0.f);   // (-0 becomes +0)
     zero = __bfloat162float(z);
     __nv_bfloat16 s = __float2bfloat16_ru(__fdiv_rn(__fsub_rn(mx, zero), 15.f));
     scale = __bfloat162float(s);
-    if (scale > 0.f && scale < 1.17549435e-38f) {   // 2^-126: the quotients below stay finite
+    if (scale > 0.f && scale < 1.17549435e-38f) {   // 2^-126: 1 / scale stays finite
         scale = 1.17549435e-38f;
         s = __float2bfloat16_rn(scale);
     }
-    return static_cast<uint32_t>(__bfloat16_as_ushort(s)) | (static_cast<uint32_t>(__bfloat16_as_ushort(z)) << 16);
+    const uint32_t word = static_cast<uint32_t>(__bfloat16_as_ushort(s)) |
+                          (static_cast<uint32_t>(__bfloat16_as_ushort(z)) << 16);
+    if (!(scale < INFINITY)) scale = zero = 0.f;
+    inv = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
+    return word;
 }
 
-// The code of x, by the definition (0 for what is not a number).
-__device__ __forceinline__ float whole_code(float x, float scale, float zero) {
-    const float n = scale > 0.f ? rintf(__fdiv_rn(__fsub_rn(x, zero), scale)) : 0.f;
-    return fminf(fmaxf(n, 0.f), 15.f);
+// The code of x, as a float whole number (inv: 1 / scale rounded, 0 where scale
+// is 0): the product with inv is at most one off, and the exact remainder says
+// whether it is, and where a tie goes (16-bit elements hit ties all the time,
+// so the product alone would not do, and a division for each costs twice this).
+__device__ __forceinline__ float whole_code(float x, float scale, float inv, float zero) {
+    const float a = __fsub_rn(x, zero);
+    const float t = fmaf(a, inv, 12582912.f);   // 1.5 2^23: the nearest whole number, in the low bits
+    const float n = t - 12582912.f;
+    const float rest = fmaf(-n, scale, a);      // exact
+    // above half a scale, or half and n odd: the next whole number on that side
+    const float limit = __int_as_float(__float_as_int(0.5f * scale) - (__float_as_int(t) & 1));
+    return fabsf(rest) > limit ? n + copysignf(1.f, rest) : n;
+}
+
+// Smaller and larger of two, not a number if one of them is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float m;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
 }
 
 // Writes lane `vec`'s vector v (dims vec * E ..) of a row into the tile of
@@ -119,20 +145,21 @@ __device__ __forceinline__ void write_row(const Vec<T>& v, uint8_t* pool, long l
         float mn = v.f[0], mx = v.f[0];
 #pragma unroll
         for (int i = 1; i < E; ++i) {
-            mn = fminf(mn, v.f[i]);
-            mx = fmaxf(mx, v.f[i]);
+            mn = min_nan(mn, v.f[i]);
+            mx = max_nan(mx, v.f[i]);
         }
 #pragma unroll
         for (int off = 1; off < kLanes; off <<= 1) {
-            mn = fminf(mn, __shfl_xor_sync(mask, mn, off));
-            mx = fmaxf(mx, __shfl_xor_sync(mask, mx, off));
+            mn = min_nan(mn, __shfl_xor_sync(mask, mn, off));
+            mx = max_nan(mx, __shfl_xor_sync(mask, mx, off));
         }
-        float scale, zero;
-        const uint32_t word = int4_group_word(mn, mx, scale, zero);
+        float scale, inv, zero;
+        const uint32_t word = int4_group_word(mn, mx, scale, inv, zero);
+        const bool finite = (word & 0x7f80u) != 0x7f80u;
         uint32_t own = 0;   // this lane's codes, four bits each
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            own |= static_cast<uint32_t>(whole_code(v.f[i], scale, zero)) << (4 * i);
+            own |= (finite ? static_cast<uint32_t>(whole_code(v.f[i], scale, inv, zero)) : 0u) << (4 * i);
         }
         // dims d and d + 8 meet in a byte: the lane 8 dims on holds the other nibble
         constexpr int kHop = 8 / E;
@@ -216,179 +243,153 @@ __global__ void __launch_bounds__(256) pa_rows_int4_kernel(const __grid_constant
     }
 }
 
-// Two neighbouring elements.
-template <typename T>
-__device__ __forceinline__ float2 load2(const T* p) {
-    if constexpr (sizeof(T) == 4) {
-        return *reinterpret_cast<const float2*>(p);
-    } else {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-        const T* e = reinterpret_cast<const T*>(&w);
-        return make_float2(to_float<T>(e[0]), to_float<T>(e[1]));
+// Transposes the 4 x 4 matrix that four neighbouring lanes (c = lane % 4) hold
+// by rows: v[j] of lane c becomes v[c] of lane j.
+__device__ __forceinline__ void transpose4(uint32_t (&v)[4], int c) {
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, (c & 1) ? v[j] : v[j + 1], 1);
+        if (c & 1) v[j] = got; else v[j + 1] = got;
     }
-}
-template <typename T>
-__device__ __forceinline__ void store2(T* p, float a, float b) {
-    if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float2*>(p) = make_float2(a, b);
-    } else {
-        uint32_t w;
-        T* e = reinterpret_cast<T*>(&w);
-        e[0] = from_float<T>(a);
-        e[1] = from_float<T>(b);
-        *reinterpret_cast<uint32_t*>(p) = w;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, (c & 2) ? v[j] : v[j + 2], 2);
+        if (c & 2) v[j] = got; else v[j + 2] = got;
     }
 }
 
 // A group of G tokens (16; 8 with 8-token blocks) whose slots fill a group of
-// the tile, one warp for one head: lane (r = lane / 4, c = lane % 4) takes
-// tokens r (and r + 8) and, of every 16 dims, 2c, 2c + 1, 2c + 8, 2c + 9, which
-// is its operand word of K; a V word is the transpose of the 8 x 8 matrix of
-// byte pairs that such words form (one movmatrix).  So a lane reads and writes
-// whole words of 16-byte vectors of the tile, where the row by row form stores
-// every byte by itself (8197 tokens: the write and read-back 53 us with it).
-//
-// The quotient is taken by the reciprocal, whose product is off by at most 3e-6
-// (15 * 1.5 * 2^-23); it rounds to the same whole number as the division's
-// unless that lies within 1e-5 of a half, and then the division is done.
+// the tile, one warp for one head, K or V: lane (r = lane / 4, m = lane % 4)
+// takes tokens r (and r + 8) and, of every 64 dims, the m-th 16, whole rows of
+// 16-byte vectors.  Its codes are its share of the four operand words of its
+// 16 dims; a 4 x 4 transpose over the lanes of a row gives each lane the words
+// it stores, one 16-byte vector of the tile.  A V word is the transpose of the
+// 8 x 8 matrix of byte pairs that K words form (one movmatrix).  Row by row,
+// every byte of the tile is a store of its own (8197 tokens: the write and the
+// read-back took 53 us with that).
 template <typename T, int D, int G>
 __device__ __forceinline__ void write_group_int4(const T* src, long long row_stride, uint8_t* tile, int B, int t0,
                                                  int lane, bool value) {
-    constexpr int NC = D / 64, NT = G / 8, W = G == 16 ? 4 : 2;
-    const int r = lane >> 2, c = lane & 3;
+    constexpr int NC = D / 64, NT = G / 8, E = Vec<T>::E;
+    const int r = lane >> 2, m = lane & 3;
     uint8_t* codes = tile + (G == 16 ? (t0 >> 4) * NC * 512 : 0);
+    uint32_t* groups = reinterpret_cast<uint32_t*>(tile + B * D / 2) + (t0 + r) * NC;
 #pragma unroll
     for (int ch = 0; ch < NC; ++ch) {
-        float2 pair[NT][4][2];   // token, 16-dim tile, dims 2c / 2c + 8
+        Vec<T> x[NT][16 / E];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    pair[t][m][u] = load2<T>(src + (r + 8 * t) * row_stride + ch * 64 + m * 16 + u * 8 + 2 * c);
-        float code[NT][4][2][2];   // token, tile, odd dim, upper: whole numbers
-        uint32_t words[NT];
+            for (int k = 0; k < 16 / E; ++k) x[t][k].load(src + (r + 8 * t) * row_stride + ch * 64 + m * 16 + k * E);
+        float sum[NT][8];   // dims d and d + 8: code + 16 code
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            float mn = pair[t][0][0].x, mx = mn;
+            float mn = x[t][0].f[0], mx = mn;
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    mn = fminf(mn, fminf(pair[t][m][u].x, pair[t][m][u].y));
-                    mx = fmaxf(mx, fmaxf(pair[t][m][u].x, pair[t][m][u].y));
-                }
+            for (int d = 1; d < 16; ++d) {
+                mn = min_nan(mn, x[t][d / E].f[d % E]);
+                mx = max_nan(mx, x[t][d / E].f[d % E]);
+            }
 #pragma unroll
             for (int off = 1; off < 4; off <<= 1) {
-                mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+                mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
             }
-            float scale, zero;
-            words[t] = int4_group_word(mn, mx, scale, zero);
-            const float inv = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
-            bool near_half = false;   // (or not a number: what is not finite must not reach another token's bytes)
+            float scale, inv, zero;
+            const uint32_t word = int4_group_word(mn, mx, scale, inv, zero);
+            const bool finite = (word & 0x7f80u) != 0x7f80u;
+            if (m == 0) groups[8 * t * NC + ch] = word;
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int odd = 0; odd < 2; ++odd) {
-                        const float q = __fmul_rn(__fsub_rn(odd ? pair[t][m][u].y : pair[t][m][u].x, zero), inv);
-                        const float n = __fsub_rn(__fadd_rn(q, 12582912.f), 12582912.f);   // 1.5 2^23: to the nearest whole
-                        near_half |= !(fabsf(q - n) <= 0.49999f);
-                        code[t][m][odd][u] = n;
-                    }
-            if (near_half) {
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int odd = 0; odd < 2; ++odd)
-                            code[t][m][odd][u] = whole_code(odd ? pair[t][m][u].y : pair[t][m][u].x, scale, zero);
+            for (int d = 0; d < 8; ++d) {
+                const float lo = whole_code(x[t][d / E].f[d % E], scale, inv, zero);
+                const float hi = whole_code(x[t][(d + 8) / E].f[d % E], scale, inv, zero);
+                sum[t][d] = finite ? fmaf(16.f, hi, lo) : 0.f;
             }
         }
-        // words: two bytes (token r and r + 8; 8-token blocks: tiles 2j and 2j + 1)
-        // of each of the two dims, summed as whole numbers below 2^16
-        uint32_t w[W];
+        // the two dims 2j, 2j + 1: a byte each in both halves of the word, token r
+        // in the lower, r + 8 in the upper (whole numbers below 2^16 in a float)
+        uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            uint32_t half[2];
-#pragma unroll
-            for (int odd = 0; odd < 2; ++odd) {
-                const float(&lo)[2] = G == 16 ? code[0][j % 4][odd] : code[0][2 * (j % 2)][odd];
-                const float(&hi)[2] = G == 16 ? code[NT - 1][j % 4][odd] : code[0][2 * (j % 2) + 1][odd];
-                const float sum = fmaf(256.f, fmaf(16.f, hi[1], hi[0]), fmaf(16.f, lo[1], lo[0]));
-                half[odd] = __float_as_uint(sum + 8388608.f);
-            }
-            w[j] = __byte_perm(half[0], half[1], 0x5410);
-            if (value) w[j] = movmatrix_trans(w[j]);
+        for (int j = 0; j < 4; ++j) {
+            const float a = G == 16 ? fmaf(256.f, sum[NT - 1][2 * j], sum[0][2 * j]) : sum[0][2 * j];
+            const float b = G == 16 ? fmaf(256.f, sum[NT - 1][2 * j + 1], sum[0][2 * j + 1]) : sum[0][2 * j + 1];
+            w[j] = __byte_perm(__float_as_uint(a + 8388608.f), __float_as_uint(b + 8388608.f), 0x5410);
         }
-        if constexpr (W == 4)
+        transpose4(w, m);   // now the words of all four 16-dim tiles, dims 2m, 2m + 1
+        if constexpr (G == 16) {
+            if (value)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = movmatrix_trans(w[j]);
             *reinterpret_cast<uint4*>(codes + (ch * 32 + lane) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-        else
-            *reinterpret_cast<uint2*>(codes + (ch * 32 + lane) * 8) = make_uint2(w[0], w[1]);
-        if (c == 0) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                *reinterpret_cast<uint32_t*>(tile + B * D / 2 + ((t0 + r + 8 * t) * NC + ch) * 4) = words[t];
+        } else {   // 8-token blocks: a word holds two tiles, the second in the upper bytes
+            uint32_t a = w[0] | (w[1] << 8), b = w[2] | (w[3] << 8);
+            if (value) {
+                a = movmatrix_trans(a);
+                b = movmatrix_trans(b);
+            }
+            *reinterpret_cast<uint2*>(codes + (ch * 32 + lane) * 8) = make_uint2(a, b);
         }
     }
 }
 
+// The way back.
 template <typename T, int D, int G>
 __device__ __forceinline__ void gather_group_int4(T* dst, long long row_stride, const uint8_t* tile, int B, int t0,
                                                   int lane, bool value) {
-    constexpr int NC = D / 64, NT = G / 8, W = G == 16 ? 4 : 2;
-    const int r = lane >> 2, c = lane & 3;
+    constexpr int NC = D / 64, NT = G / 8, E = Vec<T>::E;
+    const int r = lane >> 2, m = lane & 3;
     const uint8_t* codes = tile + (G == 16 ? (t0 >> 4) * NC * 512 : 0);
+    const uint32_t* groups = reinterpret_cast<const uint32_t*>(tile + B * D / 2) + (t0 + r) * NC;
+    uint4 raw[NC];
+    uint32_t word[NT][NC];
 #pragma unroll
     for (int ch = 0; ch < NC; ++ch) {
-        uint32_t w[W];
-        if constexpr (W == 4) {
-            const uint4 x = *reinterpret_cast<const uint4*>(codes + (ch * 32 + lane) * 16);
-            w[0] = x.x;
-            w[1] = x.y;
-            w[2] = x.z;
-            w[3] = x.w;
+        if constexpr (G == 16) {
+            raw[ch] = *reinterpret_cast<const uint4*>(codes + (ch * 32 + lane) * 16);
         } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(codes + (ch * 32 + lane) * 8);
-            w[0] = x.x;
-            w[1] = x.y;
+            const uint2 a = *reinterpret_cast<const uint2*>(codes + (ch * 32 + lane) * 8);
+            raw[ch].x = a.x;
+            raw[ch].z = a.y;
         }
-        float scale[NT], zero[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) word[t][ch] = groups[8 * t * NC + ch];
+    }
+#pragma unroll
+    for (int ch = 0; ch < NC; ++ch) {
+        uint32_t w[4] = {raw[ch].x, raw[ch].y, raw[ch].z, raw[ch].w};
+        if constexpr (G == 16) {
+            if (value)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = movmatrix_trans(w[j]);
+        } else {
+            if (value) {
+                w[0] = movmatrix_trans(w[0]);
+                w[2] = movmatrix_trans(w[2]);
+            }
+            w[1] = w[0] >> 8;
+            w[3] = w[2] >> 8;
+        }
+        transpose4(w, m);   // this lane's 16 dims: dims 2j, 2j + 1 (and 8 on) in w[j]
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const uint32_t g =
-                *reinterpret_cast<const uint32_t*>(tile + B * D / 2 + ((t0 + r + 8 * t) * NC + ch) * 4);
-            scale[t] = __uint_as_float(g << 16);
-            zero[t] = __uint_as_float(g & 0xffff0000u);
-        }
+            const float scale = __uint_as_float(word[t][ch] << 16), zero = __uint_as_float(word[t][ch] & 0xffff0000u);
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            if (value) w[j] = movmatrix_trans(w[j]);
+            for (int k = 0; k < 16 / E; ++k) {
+                Vec<T> v;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {   // bytes b and b + 2: dims 2c and 2c + 1
-                const int t = G == 16 ? b : 0, m = G == 16 ? j % 4 : 2 * (j % 2) + b;
-                T* row = dst + (r + 8 * t) * row_stride + ch * 64 + m * 16 + 2 * c;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float f[2];
-#pragma unroll
-                    for (int odd = 0; odd < 2; ++odd) {
-                        const uint32_t n = (w[j] >> (8 * b + 16 * odd + 4 * u)) & 15u;
-                        f[odd] = fmaf(scale[t], __uint_as_float(n | 0x4b000000u) - 8388608.f, zero[t]);
-                    }
-                    store2<T>(row + 8 * u, f[0], f[1]);
+                for (int e = 0; e < E; ++e) {
+                    const int d = k * E + e;   // of 16
+                    const uint32_t n = (w[d % 8 / 2] >> (8 * t + 16 * (d & 1) + 4 * (d >> 3))) & 15u;
+                    v.f[e] = fmaf(scale, __uint_as_float(n | 0x4b000000u) - 8388608.f, zero);   // (2^23 + n)
                 }
+                *reinterpret_cast<uint4*>(dst + (r + 8 * t) * row_stride + ch * 64 + m * 16 + k * E) = v.narrow();
             }
         }
     }
 }
 
-// Many tokens: a warp takes the tokens [G w, G w + G) of one head, in groups
-// where it can.  A token is part of a group if the G tokens from the one with
+// Many tokens: a warp takes the tokens [G w, G w + G) of one head's K or V, in
+// groups where it can.  A token is part of a group if the G tokens from the one with
 // offset 0 of its group in the block on (its leader) have consecutive slots;
 // a warp writes the one group whose leader it holds (another cannot start
 // within G tokens), and each of its tokens that is in no group by itself.  So a
@@ -398,14 +399,15 @@ __global__ void __launch_bounds__(128) pa_groups_int4_kernel(const __grid_consta
     wait_for_prior_work();
     constexpr int E = Vec<T>::E, V = D / E;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long unit = static_cast<long long>(blockIdx.x) * 4 + warp;   // (tokens, head), heads first
-    const long long i0 = unit / p.num_kv_heads * G;
-    const int h = static_cast<int>(unit % p.num_kv_heads);
+    const long long unit = static_cast<long long>(blockIdx.x) * 4 + warp;   // (tokens, head, K or V), the last two first
+    const long long i0 = unit / (2 * p.num_kv_heads) * G;
+    const int hs = static_cast<int>(unit % (2 * p.num_kv_heads)), h = hs >> 1;
+    const bool value = hs & 1;
     if (i0 >= p.num_tokens) return;
     // slots of the tokens i0 - G .. i0 + 2 G - 1; lane k: tokens i0 - G + k and, from the 32nd on, i0 - G + 32 + k
     auto slot_at = [&](long long i) -> long long { return i >= 0 && i < p.num_tokens ? p.slot_mapping[i] : -1; };
     const long long a = slot_at(i0 - G + lane), b = 3 * G > 32 ? slot_at(i0 - G + 32 + lane) : -1;
-    if (lane >= G && lane < 2 * G && a >= p.num_slots && h == 0) flag_error(4 /* PA_DEVERR_SLOT */);
+    if (lane >= G && lane < 2 * G && a >= p.num_slots && hs == 0) flag_error(4 /* PA_DEVERR_SLOT */);
     // bit k: token i0 - G + k has a place in the pool and its follower the next one
     long long next = __shfl_down_sync(0xffffffffu, a, 1);
     const long long first_b = __shfl_sync(0xffffffffu, b, 0), next_b = __shfl_down_sync(0xffffffffu, b, 1);
@@ -424,22 +426,18 @@ __global__ void __launch_bounds__(128) pa_groups_int4_kernel(const __grid_consta
     static_assert(2 * G <= 32 && kRun != 0, "leaders within the first 32 tokens");
     const int B = p.block_size;
     const long long stride = static_cast<long long>(p.num_kv_heads) * D;
-    T* key = reinterpret_cast<T*>(p.key) + h * D;
-    T* value = reinterpret_cast<T*>(p.value) + h * D;
+    T* rows = reinterpret_cast<T*>(value ? p.value : p.key) + h * D;
+    uint8_t* pool = value ? p.v_cache : p.k_cache;
     const uint32_t mine = static_cast<uint32_t>(groups >> G) & ((1u << G) - 1u);
     if (mine != 0u) {
         const int k = __ffs(mine) - 1;
         const long long slot = __shfl_sync(0xffffffffu, a, G + k);
         const long long block = slot / B, tile = (block * p.num_kv_heads + h) * int4_tile_bytes(B, D);
         const int t0 = static_cast<int>(slot - block * B);
-        const long long at = (i0 + k) * stride;
-        if constexpr (WRITE) {
-            write_group_int4<T, D, G>(key + at, stride, p.k_cache + tile, B, t0, lane, false);
-            write_group_int4<T, D, G>(value + at, stride, p.v_cache + tile, B, t0, lane, true);
-        } else {
-            gather_group_int4<T, D, G>(key + at, stride, p.k_cache + tile, B, t0, lane, false);
-            gather_group_int4<T, D, G>(value + at, stride, p.v_cache + tile, B, t0, lane, true);
-        }
+        if constexpr (WRITE)
+            write_group_int4<T, D, G>(rows + (i0 + k) * stride, stride, pool + tile, B, t0, lane, value);
+        else
+            gather_group_int4<T, D, G>(rows + (i0 + k) * stride, stride, pool + tile, B, t0, lane, value);
     }
     // tokens of this warp in no group: no group starts at one of the G tokens up to it
     uint32_t alone = 0u;
@@ -463,16 +461,13 @@ __global__ void __launch_bounds__(128) pa_groups_int4_kernel(const __grid_consta
         const bool live = k >= 0;
         const long long block = live ? slot / B : 0, tile = block * p.num_kv_heads + h;
         const int t = live ? static_cast<int>(slot - block * B) : 0, vec = lane % V;
-        const long long at = (i0 + (live ? k : 0)) * stride;
+        T* row = rows + (i0 + (live ? k : 0)) * stride;
         if constexpr (WRITE) {
-            Vec<T> x, y;
-            x.load(key + at + vec * E);
-            y.load(value + at + vec * E);
-            write_row<T, D, Pool::kInt4>(x, p.k_cache, tile, B, t, vec, false, 1.f, live, 0xffffffffu);
-            write_row<T, D, Pool::kInt4>(y, p.v_cache, tile, B, t, vec, true, 1.f, live, 0xffffffffu);
+            Vec<T> x;
+            x.load(row + vec * E);
+            write_row<T, D, Pool::kInt4>(x, pool, tile, B, t, vec, value, 1.f, live, 0xffffffffu);
         } else if (live) {
-            gather_row_int4<T, D>(key + at, p.k_cache + tile * int4_tile_bytes(B, D), B, t, vec, false);
-            gather_row_int4<T, D>(value + at, p.v_cache + tile * int4_tile_bytes(B, D), B, t, vec, true);
+            gather_row_int4<T, D>(row, pool + tile * int4_tile_bytes(B, D), B, t, vec, value);
         }
     }
 }
