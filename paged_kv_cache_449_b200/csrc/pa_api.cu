@@ -1078,6 +1078,8 @@ cudaError_t with_rows(pa_dtype dt, int D, F&& f) {
     }
 }
 
+int block_shift(int block_size) { return block_size == 8 ? 3 : (block_size == 16 ? 4 : 5); }
+
 pa_status check_row_shape(int64_t num_tokens, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
                           int dtype) {
     if (num_tokens < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0)
@@ -1108,7 +1110,7 @@ pa_status rows_int4(void* key, void* value, void* k_cache, void* v_cache, const 
     p.slot_mapping = slot_mapping;
     p.num_tokens = num_tokens;
     p.num_kv_heads = num_kv_heads;
-    p.block_size = block_size;
+    p.block_shift = block_shift(block_size);
     p.num_slots = num_blocks * static_cast<long long>(block_size);
     if (num_tokens > LLONG_MAX / 4096 / num_kv_heads) return PA_ERR_UNSUPPORTED;
     // Few tokens go row by row, a thread for each 16-byte vector; many by
@@ -1117,7 +1119,7 @@ pa_status rows_int4(void* key, void* value, void* k_cache, void* v_cache, const 
     const int group = block_size == 8 ? 8 : 16;
     const long long blocks = rows ? (num_tokens * num_kv_heads * (head_dim * elem_size(dtype) / 16) + 255) / 256
                                   : ((num_tokens + group - 1) / group * num_kv_heads + 1) / 2;
-    if (blocks > INT_MAX) return PA_ERR_UNSUPPORTED;
+    if (blocks > INT_MAX / 4) return PA_ERR_UNSUPPORTED;   // (the kernels' unit numbers fit 32 bits)
     const cudaError_t e = with_rows(dtype, head_dim, [&](auto tt, auto dd) -> cudaError_t {
         using T = typename decltype(tt)::type;
         constexpr int kD = decltype(dd)::value;
@@ -1182,7 +1184,7 @@ pa_status rope_and_cache(void* q_out, const void* q, const void* key, const void
     p.num_q_heads = num_q_heads;
     p.num_kv_heads = num_kv_heads;
     p.rotary_dim = rotary_dim;
-    p.block_size = block_size;
+    p.block_shift = block_shift(block_size);
     p.num_slots = num_blocks * static_cast<long long>(block_size);
     const cudaError_t e = with_rows(dtype, head_dim, [&](auto tt, auto dd) -> cudaError_t {
         using T = typename decltype(tt)::type;

@@ -40,7 +40,7 @@ struct RopeParams {
     int num_q_heads;
     int num_kv_heads;
     int rotary_dim;               // R
-    int block_size;
+    int block_shift;              // log2 of the block size
     long long num_slots;
 };
 
@@ -91,8 +91,9 @@ __global__ void __launch_bounds__(kRopeThreads, POOL == Pool::kNative ? PA_ROPE_
         turn[j] = make_float2(c * p.rope_scale, s * p.rope_scale);
     }
     if (slot >= p.num_slots && threadIdx.x == 0) flag_error(4 /* PA_DEVERR_SLOT */);
-    const long long block = live ? slot / p.block_size : 0;
-    const int t = live ? static_cast<int>(slot - block * p.block_size) : 0;
+    const int block_size = 1 << p.block_shift;
+    const long long block = live ? slot >> p.block_shift : 0;
+    const int t = live ? static_cast<int>(slot) & (block_size - 1) : 0;
     __syncthreads();
     // This thread's dims are the same in every row, and so are its angles.
     // Half layout: x' = x cos + y sin', y the pair's other element, which lies
@@ -123,8 +124,8 @@ __global__ void __launch_bounds__(kRopeThreads, POOL == Pool::kNative ? PA_ROPE_
             const long long tile = write ? block * p.num_kv_heads + h : 0;
             if (POOL == Pool::kNative && __all_sync(0xffffffffu, is_v)) {   // a warp of V rows: copied as they are
                 if (write)
-                    *reinterpret_cast<uint4*>(p.v_cache + tile * p.block_size * D * static_cast<int>(sizeof(T)) +
-                                              (vec * p.block_size + t) * 16) = raw[k];
+                    *reinterpret_cast<uint4*>(p.v_cache + tile * block_size * D * static_cast<int>(sizeof(T)) +
+                                              (vec * block_size + t) * 16) = raw[k];
                 continue;
             }
             Vec<T> x;
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kRopeThreads, POOL == Pool::kNative ? PA_ROPE_
 #pragma unroll
                 for (int off = 1; off < V; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
                 if (!is_v && w != nullptr) {
-                    const float inv = 1.f / sqrtf(sum * (1.f / D) + p.eps);
+                    const float inv = rsqrtf(sum * (1.f / D) + p.eps);
                     Vec<T> g;
                     g.load(w + vec * E);
 #pragma unroll
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kRopeThreads, POOL == Pool::kNative ? PA_ROPE_
 #pragma unroll
                 for (int e = 0; e < E; ++e) x.f[e] = to_float<T>(from_float<T>(x.f[e]));
             }
-            write_row<T, D, POOL>(x, is_v ? p.v_cache : p.k_cache, tile, p.block_size, t, vec, is_v, scale8, write,
+            write_row<T, D, POOL>(x, is_v ? p.v_cache : p.k_cache, tile, block_size, t, vec, is_v, scale8, write,
                                   0xffffffffu);
         }
         if (r0 - first + kRopeRows * kStep < rows) load(r0 + kRopeRows * kStep);

@@ -191,7 +191,7 @@ struct RowsInt4Params {
     const int64_t* slot_mapping;
     long long num_tokens;
     int num_kv_heads;
-    int block_size;
+    int block_shift;         // log2 of the block size
     long long num_slots;
 };
 
@@ -218,28 +218,27 @@ template <typename T, int D, bool WRITE>
 __global__ void __launch_bounds__(256) pa_rows_int4_kernel(const __grid_constant__ RowsInt4Params p) {
     wait_for_prior_work();
     constexpr int E = Vec<T>::E, V = D / E;
-    const long long idx = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-    const long long row = idx / V;
-    const int vec = static_cast<int>(idx % V);
-    const long long i = row / p.num_kv_heads;
-    const int h = static_cast<int>(row - i * p.num_kv_heads);
+    // (this form takes few rows: 32-bit indices; the host sees to it)
+    const int row = (blockIdx.x * 256 + threadIdx.x) / V, vec = threadIdx.x % V;
+    const int i = row / p.num_kv_heads, h = row - i * p.num_kv_heads;
     const long long slot = i < p.num_tokens ? p.slot_mapping[i] : -1;
     if (slot >= p.num_slots) flag_error(4 /* PA_DEVERR_SLOT */);
     const bool live = slot >= 0 && slot < p.num_slots;
-    const long long block = live ? slot / p.block_size : 0;
-    const int t = live ? static_cast<int>(slot - block * p.block_size) : 0;
+    const int B = 1 << p.block_shift;
+    const long long block = live ? slot >> p.block_shift : 0;
+    const int t = live ? static_cast<int>(slot) & (B - 1) : 0;
     const long long tile = block * p.num_kv_heads + h;
     if constexpr (WRITE) {
         Vec<T> k, v;
-        const long long at = live ? row * D + vec * E : 0;
+        const int at = live ? row * D + vec * E : 0;
         k.load(reinterpret_cast<const T*>(p.key) + at);
         v.load(reinterpret_cast<const T*>(p.value) + at);
-        write_row<T, D, Pool::kInt4>(k, p.k_cache, tile, p.block_size, t, vec, false, 1.f, live, 0xffffffffu);
-        write_row<T, D, Pool::kInt4>(v, p.v_cache, tile, p.block_size, t, vec, true, 1.f, live, 0xffffffffu);
+        write_row<T, D, Pool::kInt4>(k, p.k_cache, tile, B, t, vec, false, 1.f, live, 0xffffffffu);
+        write_row<T, D, Pool::kInt4>(v, p.v_cache, tile, B, t, vec, true, 1.f, live, 0xffffffffu);
     } else if (live) {
-        const long long at = tile * int4_tile_bytes(p.block_size, D);
-        gather_row_int4<T, D>(reinterpret_cast<T*>(p.key) + row * D, p.k_cache + at, p.block_size, t, vec, false);
-        gather_row_int4<T, D>(reinterpret_cast<T*>(p.value) + row * D, p.v_cache + at, p.block_size, t, vec, true);
+        const long long at = tile * int4_tile_bytes(B, D);
+        gather_row_int4<T, D>(reinterpret_cast<T*>(p.key) + row * D, p.k_cache + at, B, t, vec, false);
+        gather_row_int4<T, D>(reinterpret_cast<T*>(p.value) + row * D, p.v_cache + at, B, t, vec, true);
     }
 }
 
@@ -399,9 +398,10 @@ __global__ void __launch_bounds__(128) pa_groups_int4_kernel(const __grid_consta
     wait_for_prior_work();
     constexpr int E = Vec<T>::E, V = D / E;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long unit = static_cast<long long>(blockIdx.x) * 4 + warp;   // (tokens, head, K or V), the last two first
-    const long long i0 = unit / (2 * p.num_kv_heads) * G;
-    const int hs = static_cast<int>(unit % (2 * p.num_kv_heads)), h = hs >> 1;
+    const uint32_t unit = blockIdx.x * 4 + warp;   // (tokens, head, K or V), the last two first; below 2^32 (the host)
+    const uint32_t set = unit / (2 * p.num_kv_heads);
+    const long long i0 = static_cast<long long>(set) * G;
+    const int hs = static_cast<int>(unit - set * 2 * p.num_kv_heads), h = hs >> 1;
     const bool value = hs & 1;
     if (i0 >= p.num_tokens) return;
     // slots of the tokens i0 - G .. i0 + 2 G - 1; lane k: tokens i0 - G + k and, from the 32nd on, i0 - G + 32 + k
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(128) pa_groups_int4_kernel(const __grid_consta
 #pragma unroll
     for (int j = 0; j < G - 1; ++j) groups &= runs >> j;
     static_assert(2 * G <= 32 && kRun != 0, "leaders within the first 32 tokens");
-    const int B = p.block_size;
+    const int B = 1 << p.block_shift;
     const long long stride = static_cast<long long>(p.num_kv_heads) * D;
     T* rows = reinterpret_cast<T*>(value ? p.value : p.key) + h * D;
     uint8_t* pool = value ? p.v_cache : p.k_cache;
@@ -432,8 +432,8 @@ __global__ void __launch_bounds__(128) pa_groups_int4_kernel(const __grid_consta
     if (mine != 0u) {
         const int k = __ffs(mine) - 1;
         const long long slot = __shfl_sync(0xffffffffu, a, G + k);
-        const long long block = slot / B, tile = (block * p.num_kv_heads + h) * int4_tile_bytes(B, D);
-        const int t0 = static_cast<int>(slot - block * B);
+        const long long tile = ((slot >> p.block_shift) * p.num_kv_heads + h) * int4_tile_bytes(B, D);
+        const int t0 = static_cast<int>(slot) & (B - 1);
         if constexpr (WRITE)
             write_group_int4<T, D, G>(rows + (i0 + k) * stride, stride, pool + tile, B, t0, lane, value);
         else
@@ -459,8 +459,8 @@ __global__ void __launch_bounds__(128) pa_groups_int4_kernel(const __grid_consta
         alone = rest;
         const long long slot = __shfl_sync(0xffffffffu, a, G + (k < 0 ? 0 : k));
         const bool live = k >= 0;
-        const long long block = live ? slot / B : 0, tile = block * p.num_kv_heads + h;
-        const int t = live ? static_cast<int>(slot - block * B) : 0, vec = lane % V;
+        const long long tile = (live ? slot >> p.block_shift : 0) * p.num_kv_heads + h;
+        const int t = live ? static_cast<int>(slot) & (B - 1) : 0, vec = lane % V;
         T* row = rows + (i0 + (live ? k : 0)) * stride;
         if constexpr (WRITE) {
             Vec<T> x;
