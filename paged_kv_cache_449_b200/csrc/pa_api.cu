@@ -1132,6 +1132,12 @@ pa_status rows_int4(void* key, void* value, void* k_cache, void* v_cache, const 
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+// Threads of a token's thread block: few tokens take 256, so that each is
+// done sooner; many take 64, which wait for one another less and set up less
+// (6166 tokens of 48 rows, normed: 256 threads 52.5 us, 128 43.0, 64 42.4).
+#ifndef PA_ROPE_MANY
+#define PA_ROPE_MANY 64
+#endif
 template <pa::Pool POOL>
 pa_status rope_and_cache(void* q_out, const void* q, const void* key, const void* value, void* k_cache, void* v_cache,
                          const float* k_scale, const float* v_scale, const int64_t* positions,
@@ -1186,6 +1192,7 @@ pa_status rope_and_cache(void* q_out, const void* q, const void* key, const void
     p.rotary_dim = rotary_dim;
     p.block_shift = block_shift(block_size);
     p.num_slots = num_blocks * static_cast<long long>(block_size);
+    const int threads = num_tokens >= 8LL * sm_count() ? PA_ROPE_MANY : pa::kRopeThreads;
     const cudaError_t e = with_rows(dtype, head_dim, [&](auto tt, auto dd) -> cudaError_t {
         using T = typename decltype(tt)::type;
         constexpr int kD = decltype(dd)::value;
@@ -1195,7 +1202,7 @@ pa_status rope_and_cache(void* q_out, const void* q, const void* key, const void
                                   : (norm ? pa::pa_rope_cache_kernel<T, kD, POOL, false, true>
                                           : pa::pa_rope_cache_kernel<T, kD, POOL, false, false>);
         return launch_early(kernel,
-                            dim3(static_cast<unsigned>(num_tokens)), dim3(pa::kRopeThreads), 0,
+                            dim3(static_cast<unsigned>(num_tokens)), dim3(threads), 0,
                             static_cast<cudaStream_t>(stream), PA_EARLY_LAUNCH, p);
     });
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;

@@ -186,6 +186,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return d;
 }
 
+// The lowest n bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
 }  // namespace tc
 
 // One CTA per SM holds two tiles of 128 query rows (two consecutive tiles of
@@ -320,23 +325,29 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
         }
     }
     // Sliding window: wlo is the first key that the window of the CTA's first
-    // query reaches.  The key tiles taken are those of the sinks and those from
-    // wlo's on (nt counts them; `gap` tiles in between are left out); a block
-    // without a visible key is not fetched, whatever its table entry holds.
-    int wlo = 0, sink_tiles = INT_MAX, gap = 0;
+    // query reaches.  The key tiles are made of the blocks taken: those of the
+    // sinks, then those from wlo's on, `gap` blocks in between left out (so
+    // that a few sinks share a tile with the window's first blocks; nt counts
+    // these tiles).  A block without a visible key is not fetched, whatever its
+    // table entry holds.
+    int wlo = 0, sink_blocks = INT_MAX, gap = 0;
     if constexpr (WINDOW) {
         wlo = max(0, L - Q + tok0[0] - p.window + 1);
-        const int st = (min(p.num_sinks, L) + kKeys - 1) / kKeys;
-        if (wlo / kKeys > st) {
-            sink_tiles = st;
-            gap = wlo / kKeys - st;
+        const int sinks = min(p.num_sinks, L), sb = sinks / B + (sinks % B != 0);
+        if (wlo / B > sb) {
+            sink_blocks = sb;
+            gap = wlo / B - sb;
         }
-        nt[0] -= nt[0] > 0 ? gap : 0;
-        nt[1] -= nt[1] > 0 ? gap : 0;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            if (nt[q] > 0) nt[q] = ((L - Q + tok1[q] - 1) / B - gap) / kBlocks + 1;
     }
-    auto key_tile = [&](int j) -> int {   // the j-th key tile of this CTA
-        if constexpr (WINDOW) return j < sink_tiles ? j : j + gap;
-        return tb + j;
+    auto block_of = [&](int j, int b) -> int {   // logical block b of the j-th key tile of this CTA
+        if constexpr (WINDOW) {
+            const int i = j * kBlocks + b;
+            return i < sink_blocks ? i : i + gap;
+        }
+        return (tb + j) * kBlocks + b;
     };
     auto block_seen = [&](int jb) -> bool {   // whether any query of the CTA sees a key of block jb
         if constexpr (WINDOW) return jb * B + B > wlo || jb * B < p.num_sinks;
@@ -444,14 +455,14 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
     auto load_ids = [&](int j, int (&ids)[kBlocks]) {
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
-            const int jb = key_tile(j) * kBlocks + b;
+            const int jb = block_of(j, b);
             ids[b] = (j < ntiles && jb < nblk && block_seen(jb)) ? __ldg(table + jb) : -1;
         }
     };
     // The same mask computed by a whole warp: lane b loads block b's id (the
     // id of lane `lane` for tile j; -1 past the need), a ballot gathers them.
     auto lane_id = [&](int j) -> int {
-        const int jb = key_tile(j) * kBlocks + lane;
+        const int jb = block_of(j, lane);
         return (lane < kBlocks && j < ntiles && jb < nblk && block_seen(jb)) ? __ldg(table + jb) : -1;
     };
     auto ok_ballot = [&](int id) -> uint32_t {
@@ -482,7 +493,7 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
         if (!v_side) {
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
-                if (const int jb = key_tile(j) * kBlocks + b; jb < nblk && block_seen(jb) && !((ok >> b) & 1u))
+                if (const int jb = block_of(j, b); jb < nblk && block_seen(jb) && !((ok >> b) & 1u))
                     flag_error(1 /* PA_DEVERR_BLOCK_ID */);
             if constexpr (B == 8) {
                 // 8-token blocks: a (block, head) tile, [D/8][8][8], is already a
@@ -662,7 +673,7 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
             const int vst = j % VS;
             if (!__all_sync(0xffffffffu, tc_wait(&v_full[vst], (j / VS) & 1, abort))) break;
             if constexpr (!PREFIX) {   // (a shared prefix ends on a block boundary: no tail)
-                const int lb = (L - 1) / B - key_tile(j) * kBlocks;
+                const int lb = (L - 1) / B - gap - j * kBlocks;   // (the last block is never a sink's before a gap)
                 if (lb >= 0 && lb < kBlocks && ((ok >> lb) & 1u)) {
                     uint8_t* vt = smem + Sm::kVOff + vst * Sm::kStage + lb * kTile;
                     const int t_from = (L - 1) % B + 1;
@@ -690,8 +701,9 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
             }
             if constexpr (WINDOW) {
                 // rows before the window that no query of the CTA sees: the same
-                for (int b = 0; b < kBlocks; ++b) {
-                    const int first = (key_tile(j) * kBlocks + b) * B;
+                // (only up to the tile where the window begins)
+                for (int b = j * kBlocks <= wlo / B - gap ? 0 : kBlocks; b < kBlocks; ++b) {
+                    const int first = block_of(j, b) * B;
                     const int from = max(0, p.num_sinks - first), to = min(B, wlo - first);
                     if (from >= to || !((ok >> b) & 1u)) continue;
                     uint8_t* vt = smem + Sm::kVOff + vst * Sm::kStage + b * kTile;
@@ -742,6 +754,7 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
         // ---------------- softmax of query tile qt (thread = row = tensor-memory lane)
         const float scale = p.score_scale;
         const int row_pos = row_ok ? (PREFIX ? INT_MAX : L - Q + row_tok) : -1;
+        const int row_lo = WINDOW ? row_pos - p.window : 0;   // (the window's keys lie above it)
         const uint32_t all_blocks = (1u << kBlocks) - 1u;
         const int n = my_nt;
         uint64_t* sfull = &s_full[qt];
@@ -764,21 +777,42 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
             tc::fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(sfree);
-            const int key0 = key_tile(j) * kKeys;
+            int key0 = (tb + j) * kKeys, split = 0;   // key of column c: key0 + c (c < split, sinks before a gap: 64 j + c)
+            if constexpr (WINDOW) {
+                split = sink_blocks == INT_MAX ? 0 : (sink_blocks - j * kBlocks) * B;
+                key0 = j * kKeys + gap * B;
+            }
             // row maximum over eight independent partial maxima (no 64-long chain)
             float m8[8];
             bool all_seen = ok == all_blocks && key0 + kKeys - 1 <= row_pos;
-            if constexpr (WINDOW) all_seen = all_seen && (key0 > row_pos - p.window || key0 + kKeys <= p.num_sinks);
+            if constexpr (WINDOW) all_seen = all_seen && key0 > row_lo && split <= 0;
             if (all_seen) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) m8[c] = sv[c];
 #pragma unroll
                 for (int c = 8; c < kKeys; ++c) m8[c & 7] = fmaxf(m8[c & 7], sv[c]);
             } else {
+                uint32_t seen[2] = {0u, 0u};   // this row's keys of the tile, a bit each
+                if constexpr (WINDOW) {
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        const int k0 = key0 + 32 * w, k1 = j * kKeys + 32 * w;
+                        const uint32_t before = tc::bits_below(split - 32 * w);   // sinks before the gap
+                        seen[w] = tc::bits_below(row_pos + 1 - k0) &
+                                  (~tc::bits_below(row_lo + 1 - k0) | tc::bits_below(p.num_sinks - k0)) & ~before;
+                        seen[w] |= tc::bits_below(p.num_sinks - k1) & tc::bits_below(row_pos + 1 - k1) & before;
+#pragma unroll
+                        for (int b = 0; b < 32 / B; ++b)
+                            if (!((ok >> (w * (32 / B) + b)) & 1u)) seen[w] &= ~((B == 32 ? 0xffffffffu : (1u << (B & 31)) - 1u) << (b * B & 31));
+                    }
+                }
 #pragma unroll
                 for (int c = 0; c < kKeys; ++c) {
-                    bool vis = ((ok >> (c / B)) & 1u) && key0 + c <= row_pos;
-                    if constexpr (WINDOW) vis = vis && (key0 + c > row_pos - p.window || key0 + c < p.num_sinks);
+                    bool vis;
+                    if constexpr (WINDOW)
+                        vis = (seen[c / 32] >> (c % 32)) & 1u;
+                    else
+                        vis = ((ok >> (c / B)) & 1u) && key0 + c <= row_pos;
                     sv[c] = vis ? sv[c] : kNegInf;
                     m8[c & 7] = c < 8 ? sv[c] : fmaxf(m8[c & 7], sv[c]);
                 }

@@ -51,16 +51,16 @@ struct RopeParams {
 #define PA_ROPE_CTAS 4
 #endif
 constexpr int kRopeRows = PA_ROPE_ROWS;
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256;   // at most
 
-// One CTA per token; a group of D / E lanes takes one head's row at a time,
+// One CTA per token, of 64 threads (many tokens) to 256 (few); a group of D / E lanes takes one head's row at a time,
 // kRopeRows rows in flight: their loads are asked for first, then the token's
 // sines and cosines computed while they come.
 template <typename T, int D, Pool POOL, bool INTERLEAVED, bool NORM>
 __global__ void __launch_bounds__(kRopeThreads, POOL == Pool::kNative ? PA_ROPE_CTAS : 3) pa_rope_cache_kernel(const __grid_constant__ RopeParams p) {
     wait_for_prior_work();
     constexpr int E = Vec<T>::E, V = D / E;
-    constexpr int kStep = kRopeThreads / V;   // rows the CTA takes at once
+    const int step = blockDim.x / V;         // rows the CTA takes at once
     __shared__ float2 turn[D / 2];            // m cos, m sin
     const long long i = blockIdx.x;
     const long long slot = p.slot_mapping[i];
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kRopeThreads, POOL == Pool::kNative ? PA_ROPE_
     auto load = [&](int r0) {
 #pragma unroll
         for (int k = 0; k < kRopeRows; ++k) {
-            const int row = r0 + k * kStep;
+            const int row = r0 + k * step;
             const T* src = reinterpret_cast<const T*>(p.q) + i * p.q_stride + row * D;
             if (row >= p.num_q_heads) src = reinterpret_cast<const T*>(p.key) + i * p.k_stride + (row - p.num_q_heads) * D;
             if (row >= v_row) src = reinterpret_cast<const T*>(p.value) + i * p.v_stride + (row - v_row) * D;
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kRopeThreads, POOL == Pool::kNative ? PA_ROPE_
     };
     const int first = threadIdx.x / V;
     load(first);
-    for (int j = threadIdx.x; j < half; j += kRopeThreads) {
+    for (int j = threadIdx.x; j < half; j += blockDim.x) {
         const double turns =
             static_cast<double>(p.positions[i]) * (static_cast<double>(p.inv_freq[j]) * 0.15915494309189533577);
         const float part = static_cast<float>(turns - rint(turns));   // of a turn, [-1/2, 1/2]
@@ -113,10 +113,10 @@ __global__ void __launch_bounds__(kRopeThreads, POOL == Pool::kNative ? PA_ROPE_
     }
 
     // every lane of a warp takes the same number of turns: the shuffles stay whole
-    for (int r0 = first; r0 - first < rows; r0 += kRopeRows * kStep) {
+    for (int r0 = first; r0 - first < rows; r0 += kRopeRows * step) {
 #pragma unroll
         for (int k = 0; k < kRopeRows; ++k) {
-            const int row = r0 + k * kStep;
+            const int row = r0 + k * step;
             if (row - first >= rows) break;   // (uniform)
             const bool in = row < rows, is_q = row < p.num_q_heads, is_v = row >= v_row;
             const int h = is_q ? row : (is_v ? row - v_row : row - p.num_q_heads);
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kRopeThreads, POOL == Pool::kNative ? PA_ROPE_
             write_row<T, D, POOL>(x, is_v ? p.v_cache : p.k_cache, tile, block_size, t, vec, is_v, scale8, write,
                                   0xffffffffu);
         }
-        if (r0 - first + kRopeRows * kStep < rows) load(r0 + kRopeRows * kStep);
+        if (r0 - first + kRopeRows * step < rows) load(r0 + kRopeRows * step);
     }
 }
 
