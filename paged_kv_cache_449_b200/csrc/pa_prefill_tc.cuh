@@ -328,9 +328,9 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
     // query reaches.  The key tiles are made of the blocks taken: those of the
     // sinks, then those from wlo's on, `gap` blocks in between left out (so
     // that a few sinks share a tile with the window's first blocks; nt counts
-    // these tiles).  A block without a visible key is not fetched, whatever its
-    // table entry holds.
-    int wlo = 0, sink_blocks = INT_MAX, gap = 0;
+    // these tiles).  Every block taken holds a key that some query sees; the
+    // others' table entries are not looked at.
+    int wlo = 0, sink_blocks = 0, gap = 0;   // (sink_blocks: those before a gap)
     if constexpr (WINDOW) {
         wlo = max(0, L - Q + tok0[0] - p.window + 1);
         const int sinks = min(p.num_sinks, L), sb = sinks / B + (sinks % B != 0);
@@ -348,10 +348,6 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
             return i < sink_blocks ? i : i + gap;
         }
         return (tb + j) * kBlocks + b;
-    };
-    auto block_seen = [&](int jb) -> bool {   // whether any query of the CTA sees a key of block jb
-        if constexpr (WINDOW) return jb * B + B > wlo || jb * B < p.num_sinks;
-        return true;
     };
     // Shared-prefix form, the CTA's last step: its sequences [tok0[0], seq_end)
     // arrive on their (sequence, kv head) counters once its partials are
@@ -452,18 +448,25 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
     // ---- block ids of key tile j, and which of them may be fetched (every role
     //      derives the same mask from the table)
     const int32_t* table = p.block_tables + static_cast<long long>(s) * p.max_blocks_per_seq;
+    const int nseen = nblk - (WINDOW ? gap : tb * kBlocks);   // blocks of this CTA's key tiles
     auto load_ids = [&](int j, int (&ids)[kBlocks]) {
+        const int32_t* row = table + (tb + j) * kBlocks + gap;   // (gap: 0 without a window)
+        if (WINDOW && j * kBlocks < sink_blocks) {   // a tile of sinks, or of sinks and the window's first blocks
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            const int jb = block_of(j, b);
-            ids[b] = (j < ntiles && jb < nblk && block_seen(jb)) ? __ldg(table + jb) : -1;
+            for (int b = 0; b < kBlocks; ++b)
+                ids[b] = j * kBlocks + b < nseen ? __ldg(row + b - (j * kBlocks + b < sink_blocks ? gap : 0)) : -1;
+            return;
         }
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+            ids[b] = (j < ntiles && j * kBlocks + b < nseen) ? __ldg(row + b) : -1;
     };
     // The same mask computed by a whole warp: lane b loads block b's id (the
     // id of lane `lane` for tile j; -1 past the need), a ballot gathers them.
     auto lane_id = [&](int j) -> int {
-        const int jb = block_of(j, lane);
-        return (lane < kBlocks && j < ntiles && jb < nblk && block_seen(jb)) ? __ldg(table + jb) : -1;
+        const int i = j * kBlocks + lane;
+        return (lane < kBlocks && j < ntiles && i < nseen)
+                   ? __ldg(table + tb * kBlocks + i + (WINDOW && i >= sink_blocks ? gap : 0)) : -1;
     };
     auto ok_ballot = [&](int id) -> uint32_t {
         return __ballot_sync(0xffffffffu, id >= 0 && static_cast<long long>(id) < p.num_blocks);
@@ -493,8 +496,7 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
         if (!v_side) {
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
-                if (const int jb = block_of(j, b); jb < nblk && block_seen(jb) && !((ok >> b) & 1u))
-                    flag_error(1 /* PA_DEVERR_BLOCK_ID */);
+                if (j * kBlocks + b < nseen && !((ok >> b) & 1u)) flag_error(1 /* PA_DEVERR_BLOCK_ID */);
             if constexpr (B == 8) {
                 // 8-token blocks: a (block, head) tile, [D/8][8][8], is already a
                 // column of core matrices of the S MMA's K-major operand, so the
@@ -754,7 +756,13 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
         // ---------------- softmax of query tile qt (thread = row = tensor-memory lane)
         const float scale = p.score_scale;
         const int row_pos = row_ok ? (PREFIX ? INT_MAX : L - Q + row_tok) : -1;
-        const int row_lo = WINDOW ? row_pos - p.window : 0;   // (the window's keys lie above it)
+        // the tiles that this row sees whole, first to last (a window's: keys above row_pos - window)
+        int whole0 = 0, whole1 = 0;
+        if constexpr (WINDOW) {
+            const int above = max(0, row_pos - p.window + 1 - gap * B);
+            whole0 = max((above + kKeys - 1) / kKeys, (sink_blocks + kBlocks - 1) / kBlocks);
+            whole1 = (row_pos + 1 - gap * B) / kKeys - 1;   // (row_pos + 1 >= gap * B, or the row is none)
+        }
         const uint32_t all_blocks = (1u << kBlocks) - 1u;
         const int n = my_nt;
         uint64_t* sfull = &s_full[qt];
@@ -777,16 +785,10 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
             tc::fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(sfree);
-            int key0 = (tb + j) * kKeys, split = 0;   // key of column c: key0 + c (c < split, sinks before a gap: 64 j + c)
-            if constexpr (WINDOW) {
-                split = sink_blocks == INT_MAX ? 0 : (sink_blocks - j * kBlocks) * B;
-                key0 = j * kKeys + gap * B;
-            }
+            const int key0 = (tb + j) * kKeys;
             // row maximum over eight independent partial maxima (no 64-long chain)
             float m8[8];
-            bool all_seen = ok == all_blocks && key0 + kKeys - 1 <= row_pos;
-            if constexpr (WINDOW) all_seen = all_seen && key0 > row_lo && split <= 0;
-            if (all_seen) {
+            if (ok == all_blocks && (WINDOW ? j >= whole0 && j <= whole1 : key0 + kKeys - 1 <= row_pos)) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) m8[c] = sv[c];
 #pragma unroll
@@ -794,9 +796,12 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
             } else {
                 uint32_t seen[2] = {0u, 0u};   // this row's keys of the tile, a bit each
                 if constexpr (WINDOW) {
+                    // key of column c: 64 j + c for the sinks before a gap (c < split), gap blocks further on after
+                    const int split = (sink_blocks - j * kBlocks) * B;
+                    const int row_lo = row_pos - p.window;
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
-                        const int k0 = key0 + 32 * w, k1 = j * kKeys + 32 * w;
+                        const int k1 = j * kKeys + 32 * w, k0 = k1 + gap * B;
                         const uint32_t before = tc::bits_below(split - 32 * w);   // sinks before the gap
                         seen[w] = tc::bits_below(row_pos + 1 - k0) &
                                   (~tc::bits_below(row_lo + 1 - k0) | tc::bits_below(p.num_sinks - k0)) & ~before;
