@@ -277,7 +277,9 @@ int sm_count() {
 template <bool SPLIT, bool FP8 = false, bool PREFIX = false, bool WINDOW = false>
 cudaError_t decode_dispatch(pa_dtype dt, int D, int B, const pa::DecodeParams& p, dim3 grid, cudaStream_t st) {
     const long long ctas = static_cast<long long>(grid.x) * grid.y * grid.z;
-    const bool deep = !SPLIT && ctas <= static_cast<long long>(PA_DEEP_MAX_CTAS_PER_SM) * sm_count();
+    // (partitions of a window: deep where the SMs hold them all at once)
+    const bool deep = SPLIT ? WINDOW && ctas <= sm_count()
+                            : ctas <= static_cast<long long>(PA_DEEP_MAX_CTAS_PER_SM) * sm_count();
     return with_variant(dt, D, B, [&](auto tt, auto dd, auto bb) -> cudaError_t {
         using T = typename decltype(tt)::type;
         constexpr int kD = decltype(dd)::value, kB = decltype(bb)::value;
@@ -287,6 +289,8 @@ cudaError_t decode_dispatch(pa_dtype dt, int D, int B, const pa::DecodeParams& p
             return deep ? launch_decode<T, kD, kB, false, Kind::kDeep, false, true>(p, grid, st)
                         : launch_decode<T, kD, kB, false, Kind::kWide, false, true>(p, grid, st);
         } else if constexpr (SPLIT) {
+            if constexpr (WINDOW)
+                if (deep) return launch_decode<T, kD, kB, true, Kind::kDeep, FP8, false, true>(p, grid, st);
             return launch_decode<T, kD, kB, true, Kind::kWide, FP8, false, WINDOW>(p, grid, st);
         } else {
             return deep ? launch_decode<T, kD, kB, false, Kind::kDeep, FP8, false, WINDOW>(p, grid, st)
@@ -986,17 +990,30 @@ long long window_partitions(long long units, int unit, int partition_size) {
 }
 
 // A partition size for units of `unit` tokens visible to each (sequence, kv
-// head): the work over the SMs once, between `least` and `enough` tokens (a
-// partition costs its thread block's start and its merge, so a batch that
-// fills the device takes no smaller ones), and more where that would be over
-// 16 partitions an SM.  0: one pass.
-int choose_partition(long long seqs, int num_kv_heads, long long units, int unit, int least, int enough) {
-    const long long tokens = units * unit, pairs = seqs * num_kv_heads, sms = std::max(1, sm_count());
+// head): as many partitions as leave every SM one deep thread block, of 256
+// tokens at least; 0, one pass, where the sequences alone do.  A window over
+// 16-bit pools, two sequences of 4 kv heads, 4096 tokens visible: one pass 14.7
+// us, 17 partitions 8.9; 16 of 8 heads, 1024 visible: one pass 15.2, two
+// partitions (more thread blocks than SMs, so wide ones) 22.
+int choose_deep_partition(long long pairs, long long units, int unit) {
     if (pairs <= 0 || units <= 0) return 0;
+    const long long parts = std::max(1, sm_count()) / pairs;
+    if (parts < 2) return 0;
+    const long long step = std::max(16, unit), tokens = units * unit;
+    const long long size = std::max<long long>(((tokens + parts - 1) / parts + step - 1) / step * step, 256);
+    return size >= tokens || size > INT_MAX / 2 ? 0 : static_cast<int>(size);
+}
+
+// 4-bit pools: the same while the SMs hold the (sequence, kv head) pairs twice
+// (one 32k sequence of 8 heads: 15.8 us, 19.5 in wide blocks of 1024 tokens) or
+// contexts are short; beyond, partitions for wide blocks: 2048 tokens (one's
+// start and merge cost as much as 100 tokens a warp), more where that would be
+// over 16 an SM.
+int choose_int4_partition(long long pairs, long long units, int unit) {
+    const long long sms = std::max(1, sm_count()), tokens = units * unit;
+    if (2 * pairs <= sms || (pairs <= sms && tokens <= 4096)) return choose_deep_partition(pairs, units, unit);
     const long long work = tokens > LLONG_MAX / pairs ? LLONG_MAX : tokens * pairs;
-    long long size = std::max(work / (16 * sms), std::min<long long>(std::max<long long>(work / sms, least), enough));
-    const long long step = std::max(16, unit);   // partition sizes: multiples of both 16 and the block
-    size = (size + step - 1) / step * step;
+    const long long size = (std::max<long long>(work / (16 * sms), 2048) + unit - 1) / unit * unit;
     return size >= tokens || size > INT_MAX / 2 ? 0 : static_cast<int>(size);
 }
 
@@ -1208,17 +1225,22 @@ pa_status rope_and_cache(void* q_out, const void* q, const void* key, const void
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// CTAs of the 4-bit decode: 4 warps, four CTAs per SM, each warp with a ring
-// of 32-token stages (13.8 KB; 9/8 bytes an element of K and V).
-#ifndef PA_INT4_WARPS
-#define PA_INT4_WARPS 4
-#endif
-#ifndef PA_INT4_RING
-#define PA_INT4_RING 13824
-#endif
+// Thread blocks of the 4-bit decode: 4 warps, or 12 where the SMs hold one each
+// of all of them (deep); each warp with a ring of 32-token stages (13.8 KB; 9/8
+// bytes an element of K and V).
+constexpr int kInt4WideWarps = 4, kInt4DeepWarps = 12;
 constexpr int kInt4Step = 32;
 template <int D>
-constexpr int kInt4Stages = PA_INT4_RING / (2 * pa::int4_tile_bytes(kInt4Step, D));
+constexpr int kInt4Stages = 13824 / (2 * pa::int4_tile_bytes(kInt4Step, D));
+
+template <typename T, int D, int B, int NW>
+cudaError_t launch_int4(const pa::DecodeParams& p, dim3 grid, cudaStream_t stream) {
+    auto kernel = pa::pa_decode_int4_kernel<T, D, B, NW, kInt4Stages<D>>;
+    const cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel));
+    if (e != cudaSuccess) return e;
+    return launch_early(kernel, grid, dim3(NW * 32), pa::Int4Smem<D, B, NW, kInt4Stages<D>>::kTotal, stream,
+                        PA_EARLY_LAUNCH, p);
+}
 
 }  // namespace
 
@@ -1282,7 +1304,7 @@ pa_status pa_decode_int4_plan(int num_seqs, int num_q_heads, int num_kv_heads, i
         max_context_len < 0 || *partition_size < -1 || check_window(window, num_sinks, 0) != PA_OK)
         return PA_ERR_INVALID_ARG;
     const long long units = visible_units(max_context_len, window, num_sinks, kInt4Step);
-    if (*partition_size < 0) *partition_size = choose_partition(num_seqs, num_kv_heads, units, kInt4Step, 128, 1024);
+    if (*partition_size < 0) *partition_size = choose_int4_partition(static_cast<long long>(num_seqs) * num_kv_heads, units, kInt4Step);
     if (*partition_size % kInt4Step != 0) return PA_ERR_INVALID_ARG;
     const long long parts = window_partitions(units, kInt4Step, *partition_size);
     *bytes = parts > 1 ? splitk_bytes(num_seqs, num_q_heads, parts, head_dim) : 0;
@@ -1315,18 +1337,15 @@ pa_status pa_decode_int4(void* out, const void* q, const void* k_cache, const vo
     if (st != PA_OK) return st;
     p.partition_blocks = parts > 1 ? partition_size / kInt4Step : INT_MAX / 2;
     const dim3 grid(static_cast<unsigned>(std::max(1LL, parts)), num_kv_heads, num_seqs);
+    const bool deep = std::max(1LL, parts) * num_kv_heads * num_seqs <= sm_count();
     const cudaError_t e = with_variant(dtype, head_dim, block_size, [&](auto tt, auto dd, auto bb) -> cudaError_t {
         using T = typename decltype(tt)::type;
         constexpr int kD = decltype(dd)::value, kB = decltype(bb)::value;
         if constexpr (pa::IsF32<T>::value) {
             return cudaErrorInvalidValue;
         } else {
-            auto kernel = pa::pa_decode_int4_kernel<T, kD, kB, PA_INT4_WARPS, kInt4Stages<kD>>;
-            const cudaError_t fit = ensure_smem(reinterpret_cast<const void*>(kernel));
-            if (fit != cudaSuccess) return fit;
-            return launch_early(kernel, grid, dim3(PA_INT4_WARPS * 32),
-                                pa::Int4Smem<kD, kB, PA_INT4_WARPS, kInt4Stages<kD>>::kTotal,
-                                static_cast<cudaStream_t>(stream), PA_EARLY_LAUNCH, p);
+            return deep ? launch_int4<T, kD, kB, kInt4DeepWarps>(p, grid, static_cast<cudaStream_t>(stream))
+                        : launch_int4<T, kD, kB, kInt4WideWarps>(p, grid, static_cast<cudaStream_t>(stream));
         }
     });
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
@@ -1340,7 +1359,7 @@ pa_status pa_decode_window_plan(int num_seqs, int num_q_heads, int num_kv_heads,
         return PA_ERR_INVALID_ARG;
     const long long units = visible_units(max_context_len, window, num_sinks, block_size);
     if (*partition_size < 0)
-        *partition_size = choose_partition(num_seqs, num_kv_heads, units, block_size, 128, 1024);
+        *partition_size = choose_deep_partition(static_cast<long long>(num_seqs) * num_kv_heads, units, block_size);
     if (*partition_size % 16 != 0 || *partition_size % block_size != 0) return PA_ERR_INVALID_ARG;
     const long long parts = window_partitions(units, block_size, *partition_size);
     *bytes = parts > 1 ? splitk_bytes(num_seqs, num_q_heads, parts, head_dim) : 0;

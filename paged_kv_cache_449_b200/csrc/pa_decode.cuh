@@ -203,6 +203,88 @@ __device__ __forceinline__ void merge_partitions_cta(const DecodeParams& p, int 
     }
 }
 
+// Four output values x * inv, rounded once.
+template <typename T>
+__device__ __forceinline__ void store4(T* dst, const float4& x, float inv) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(dst) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    } else {
+        uint2 w;
+        T* e = reinterpret_cast<T*>(&w);
+        e[0] = from_float<T>(x.x * inv);
+        e[1] = from_float<T>(x.y * inv);
+        e[2] = from_float<T>(x.z * inv);
+        e[3] = from_float<T>(x.w * inv);
+        *reinterpret_cast<uint2*>(dst) = w;
+    }
+}
+
+// The log-sum-exp merge of the np partials of (sequence, kv head) by one CTA:
+// first every partial's weight (a warp per head, lanes over partials, into
+// `weights`), then the weighted sums, eight partials' loads in flight a
+// thread.  The partials were written by other CTAs: read past L1.  More than
+// `room` weights go by merge_partitions_cta, one partial after the other.
+template <typename T, int D, bool LOG2, int THREADS>
+__device__ __forceinline__ void merge_partials(const DecodeParams& p, int s, int kvh, int np, float* weights, int room) {
+    const int group = p.group;
+    if (static_cast<long long>(group) * np > room) {
+        merge_partitions_cta<T, D, LOG2, THREADS>(p, s, kvh, np);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long row0 = static_cast<long long>(s) * p.num_q_heads + kvh * group;
+    for (int h = warp; h < group; h += THREADS / 32) {
+        const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + (row0 + h) * p.num_partitions;
+        float M = kNegInf;
+        for (int q = lane; q < np; q += 32) {
+            const float m = __ldcg(ml + q).x;
+            weights[h * np + q] = m;
+            M = fmaxf(M, m);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        const float top = M == kNegInf ? 0.f : M;
+        float den = 0.f;
+        for (int q = lane; q < np; q += 32) {
+            const float w = softmax_exp<LOG2>(weights[h * np + q] - top);
+            weights[h * np + q] = w;
+            den = fmaf(w, __ldcg(ml + q).y, den);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
+        const float inv = den > 0.f ? 1.f / den : 0.f;
+        for (int q = lane; q < np; q += 32) weights[h * np + q] *= inv;
+    }
+    __syncthreads();
+    for (int v = threadIdx.x; v < group * (D / 4); v += THREADS) {
+        const int h = v / (D / 4), c = v % (D / 4);
+        const float4* acc = reinterpret_cast<const float4*>(p.part_acc + (row0 + h) * p.num_partitions * D) + c;
+        const float* w = weights + h * np;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        int q = 0;
+        for (; q + 8 <= np; q += 8) {
+            float4 x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = __ldcg(acc + static_cast<long long>(q + k) * (D / 4));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                a.x = fmaf(w[q + k], x[k].x, a.x);
+                a.y = fmaf(w[q + k], x[k].y, a.y);
+                a.z = fmaf(w[q + k], x[k].z, a.z);
+                a.w = fmaf(w[q + k], x[k].w, a.w);
+            }
+        }
+        for (; q < np; ++q) {
+            const float4 x = __ldcg(acc + static_cast<long long>(q) * (D / 4));
+            a.x = fmaf(w[q], x.x, a.x);
+            a.y = fmaf(w[q], x.y, a.y);
+            a.z = fmaf(w[q], x.z, a.z);
+            a.w = fmaf(w[q], x.w, a.w);
+        }
+        store4<T>(reinterpret_cast<T*>(p.out) + (row0 + h) * D + 4 * c, a, 1.f);
+    }
+}
+
 
 template <typename T, int D, int B, int NW, int STAGES, bool FP8 = false>
 struct DecodeSmem {
@@ -640,9 +722,11 @@ __global__ void __launch_bounds__(NW * 32, (PREFIX && NW <= 4) ? PA_PREFIX_MIN_C
             // (shared-prefix form: the last of the prefix pass's partitions
             // and this pass, whichever kernel it runs in).
             __shared__ int last_arrival;
-            __threadfence();
+            if constexpr (!WINDOW) __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) {
+                // (the barrier orders the CTA's writes before thread 0's fence, which covers them)
+                if constexpr (WINDOW) __threadfence();
                 const int old = atomicAdd(p.counters + static_cast<long long>(s) * p.num_kv_heads + kvh, 1);
                 last_arrival = old == num_parts - 1;
             }
@@ -657,6 +741,9 @@ __global__ void __launch_bounds__(NW * 32, (PREFIX && NW <= 4) ? PA_PREFIX_MIN_C
                         const bool use[1] = {true}, zero[1] = {refused};
                         merge_shared_prefix<T, D, 1>(p.out, p.part_acc, p.part_ml, num_parts, row, c, use, zero);
                     }
+                } else if constexpr (WINDOW) {
+                    merge_partials<T, D, kLog2, NW * 32>(p, s, kvh, num_parts, reinterpret_cast<float*>(smem),
+                                                         Smem::kArea / 4);
                 } else {
                     merge_partitions_cta<T, D, kLog2, NW * 32>(p, s, kvh, num_parts);
                 }
