@@ -74,9 +74,9 @@ pa_status pa_rope_and_cache_int4(void* q_out, const void* q, const void* key, co
  * and kv head) share a scale and a zero, both bf16:
  *     zero  = the group's minimum rounded down to bf16
  *     scale = (maximum - zero) / 15 rounded up to bf16 (0 if that is 0, else at least 2^-126)
- *     code  = (x - zero) / scale to the nearest whole number, ties to even, in 0..15 (0 where scale is 0)
+ *     code  = (x - zero) / scale rounded to the nearest whole number, ties to even, in 0..15 (0 where scale is 0)
  *     value = zero + scale * code
- * in fp32 (the difference x - zero rounded, its quotient exact).  A group that is
+ * every step in fp32.  A group that is
  * not finite, or whose span is not, reads back as values that are not finite.  Pools are byte arrays of (block, kv head) tiles of
  * block_size * head_dim * 9 / 16 bytes:
  *   codes   block_size * head_dim / 2 bytes.  A byte holds dims d (low nibble)

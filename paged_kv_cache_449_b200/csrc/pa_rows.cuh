@@ -9,9 +9,9 @@
 // scale and a zero:
 //     zero  = the group's minimum rounded down to bf16
 //     scale = (maximum - zero) / 15 rounded up to bf16 (0 if that is 0, else at least 2^-126)
-//     code  = (x - zero) / scale to the nearest whole number, ties to even, in 0..15
+//     code  = (x - zero) / scale rounded to the nearest whole number, ties to even, in 0..15
 //     value = zero + scale * code
-// (in fp32, the quotient of the fp32 difference exact).  The roundings outwards keep the whole group inside
+// (every step in fp32).  The roundings outwards keep the whole group inside
 // [zero, zero + 15 scale], so no value is clipped by more than fp32's own
 // rounding; bf16 covers every input type's range, where fp16 would not.
 // Groups of 64 dims cost 4 bytes per 32 bytes of codes.
@@ -88,18 +88,18 @@ __device__ __forceinline__ uint32_t int4_group_word(float mn, float mx, float& s
     return word;
 }
 
-// The code of x, as a float whole number (inv: 1 / scale rounded, 0 where scale
-// is 0): the product with inv is at most one off, and the exact remainder says
-// whether it is, and where a tie goes (16-bit elements hit ties all the time,
-// so the product alone would not do, and a division for each costs twice this).
-__device__ __forceinline__ float whole_code(float x, float scale, float inv, float zero) {
+// The code of x in the low bits (four, of a finite group) of the result.  inv
+// is 1 / scale rounded (0 where scale is 0): the product with it, corrected once
+// by the exact remainder, is the rounded quotient (P. Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990), so the
+// code is the division's; the sum with 1.5 * 2^23 rounds it to a whole number.
+// (The plain product is off next to ties, which 16-bit elements hit all the
+// time; a division for each element costs twice this.)
+__device__ __forceinline__ uint32_t code_bits(float x, float scale, float inv, float zero) {
     const float a = __fsub_rn(x, zero);
-    const float t = fmaf(a, inv, 12582912.f);   // 1.5 2^23: the nearest whole number, in the low bits
-    const float n = t - 12582912.f;
-    const float rest = fmaf(-n, scale, a);      // exact
-    // above half a scale, or half and n odd: the next whole number on that side
-    const float limit = __int_as_float(__float_as_int(0.5f * scale) - (__float_as_int(t) & 1));
-    return fabsf(rest) > limit ? n + copysignf(1.f, rest) : n;
+    const float q = __fmul_rn(a, inv);
+    const float quotient = fmaf(fmaf(-q, scale, a), inv, q);
+    return __float_as_uint(__fadd_rn(quotient, 12582912.f));
 }
 
 // Smaller and larger of two, not a number if one of them is.
@@ -159,7 +159,7 @@ __device__ __forceinline__ void write_row(const Vec<T>& v, uint8_t* pool, long l
         uint32_t own = 0;   // this lane's codes, four bits each
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            own |= (finite ? static_cast<uint32_t>(whole_code(v.f[i], scale, inv, zero)) : 0u) << (4 * i);
+            own |= (finite ? code_bits(v.f[i], scale, inv, zero) & 15u : 0u) << (4 * i);
         }
         // dims d and d + 8 meet in a byte: the lane 8 dims on holds the other nibble
         constexpr int kHop = 8 / E;
@@ -273,21 +273,29 @@ __device__ __forceinline__ void write_group_int4(const T* src, long long row_str
     const int r = lane >> 2, m = lane & 3;
     uint8_t* codes = tile + (G == 16 ? (t0 >> 4) * NC * 512 : 0);
     uint32_t* groups = reinterpret_cast<uint32_t*>(tile + B * D / 2) + (t0 + r) * NC;
+    // every load first: 16 dims of a row are 16 / E vectors
+    uint4 raw[NC][NT][16 / E];
 #pragma unroll
-    for (int ch = 0; ch < NC; ++ch) {
-        Vec<T> x[NT][16 / E];
+    for (int ch = 0; ch < NC; ++ch)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int k = 0; k < 16 / E; ++k) x[t][k].load(src + (r + 8 * t) * row_stride + ch * 64 + m * 16 + k * E);
-        float sum[NT][8];   // dims d and d + 8: code + 16 code
+            for (int k = 0; k < 16 / E; ++k)
+                raw[ch][t][k] = *reinterpret_cast<const uint4*>(src + (r + 8 * t) * row_stride + ch * 64 + m * 16 + k * E);
+#pragma unroll
+    for (int ch = 0; ch < NC; ++ch) {
+        uint32_t byte[NT][8];   // dims d and d + 8 in the lowest byte
+        uint32_t keep = 0u;     // the bytes of finite groups
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            float mn = x[t][0].f[0], mx = mn;
+            Vec<T> x[16 / E];
+#pragma unroll
+            for (int k = 0; k < 16 / E; ++k) x[k].widen(raw[ch][t][k]);
+            float mn = x[0].f[0], mx = mn;
 #pragma unroll
             for (int d = 1; d < 16; ++d) {
-                mn = min_nan(mn, x[t][d / E].f[d % E]);
-                mx = max_nan(mx, x[t][d / E].f[d % E]);
+                mn = min_nan(mn, x[d / E].f[d % E]);
+                mx = max_nan(mx, x[d / E].f[d % E]);
             }
 #pragma unroll
             for (int off = 1; off < 4; off <<= 1) {
@@ -296,23 +304,23 @@ __device__ __forceinline__ void write_group_int4(const T* src, long long row_str
             }
             float scale, inv, zero;
             const uint32_t word = int4_group_word(mn, mx, scale, inv, zero);
-            const bool finite = (word & 0x7f80u) != 0x7f80u;
+            if ((word & 0x7f80u) != 0x7f80u) keep |= G == 16 ? 0x00ff00ffu << (8 * t) : 0xffffffffu;
             if (m == 0) groups[8 * t * NC + ch] = word;
 #pragma unroll
-            for (int d = 0; d < 8; ++d) {
-                const float lo = whole_code(x[t][d / E].f[d % E], scale, inv, zero);
-                const float hi = whole_code(x[t][(d + 8) / E].f[d % E], scale, inv, zero);
-                sum[t][d] = finite ? fmaf(16.f, hi, lo) : 0.f;
-            }
+            for (int d = 0; d < 8; ++d)
+                byte[t][d] = code_bits(x[d / E].f[d % E], scale, inv, zero) +
+                             (code_bits(x[(d + 8) / E].f[d % E], scale, inv, zero) << 4);
         }
         // the two dims 2j, 2j + 1: a byte each in both halves of the word, token r
-        // in the lower, r + 8 in the upper (whole numbers below 2^16 in a float)
+        // in the lower, r + 8 in the upper
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float a = G == 16 ? fmaf(256.f, sum[NT - 1][2 * j], sum[0][2 * j]) : sum[0][2 * j];
-            const float b = G == 16 ? fmaf(256.f, sum[NT - 1][2 * j + 1], sum[0][2 * j + 1]) : sum[0][2 * j + 1];
-            w[j] = __byte_perm(__float_as_uint(a + 8388608.f), __float_as_uint(b + 8388608.f), 0x5410);
+            if constexpr (G == 16)
+                w[j] = __byte_perm(__byte_perm(byte[0][2 * j], byte[NT - 1][2 * j], 0x0040),
+                                   __byte_perm(byte[0][2 * j + 1], byte[NT - 1][2 * j + 1], 0x0040), 0x5410) & keep;
+            else
+                w[j] = __byte_perm(byte[0][2 * j], byte[0][2 * j + 1], 0x0400) & keep & 0x00ff00ffu;
         }
         transpose4(w, m);   // now the words of all four 16-dim tiles, dims 2m, 2m + 1
         if constexpr (G == 16) {

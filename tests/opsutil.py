@@ -50,8 +50,8 @@ def quantise4(x):
     scale = bf16_towards((y.max(-1) - zero) / np.float32(15), True)
     scale = np.where((scale > 0) & (scale < 2.0 ** -126), np.float32(2.0 ** -126), scale)
     with np.errstate(all="ignore"):
-        part = (y - zero[..., None]).astype(np.float64) / scale[..., None]
-    part = np.where(scale[..., None] > 0, part, 0.0)
+        part = (y - zero[..., None]) / scale[..., None]
+    part = np.where(scale[..., None] > 0, part, np.float32(0))
     return np.clip(np.rint(part), 0, 15).astype(np.uint8).reshape(x.shape), scale, zero
 
 
