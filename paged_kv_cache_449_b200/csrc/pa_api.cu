@@ -1107,9 +1107,11 @@ pa_status check_row_shape(int64_t num_tokens, int num_kv_heads, int head_dim, in
     return PA_OK;
 }
 
-#ifndef PA_INT4_FEW_ROWS
-#define PA_INT4_FEW_ROWS 2048
-#endif
+// At most this many rows (tokens x kv heads) go one by one.  A write of 8 heads,
+// one by one / by groups: 256 tokens 2.8 / 2.6 us in order, 2.8 / 6.4 at
+// scattered slots; 512 tokens 3.7 / 2.7 and 3.7 / 6.4; 4096 tokens 13.4 / 6.8 and
+// 13.4 / 16.5.  Scattered slots are a decode step's, seldom over 512 sequences.
+constexpr long long kInt4FewRows = 4096;
 template <bool WRITE>
 pa_status rows_int4(void* key, void* value, void* k_cache, void* v_cache, const int64_t* slot_mapping,
                     int64_t num_tokens, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
@@ -1130,9 +1132,9 @@ pa_status rows_int4(void* key, void* value, void* k_cache, void* v_cache, const 
     p.block_shift = block_shift(block_size);
     p.num_slots = num_blocks * static_cast<long long>(block_size);
     if (num_tokens > LLONG_MAX / 4096 / num_kv_heads) return PA_ERR_UNSUPPORTED;
-    // Few tokens go row by row, a thread for each 16-byte vector; many by
-    // groups of a block's tokens, a warp for each (PA_INT4_ROWS_TOKENS).
-    const bool rows = num_tokens * num_kv_heads <= PA_INT4_FEW_ROWS;
+    // Few rows go one by one, a thread for each 16-byte vector; many by groups
+    // of a block's tokens, a warp for each.
+    const bool rows = num_tokens * num_kv_heads <= kInt4FewRows;
     const int group = block_size == 8 ? 8 : 16;
     const long long blocks = rows ? (num_tokens * num_kv_heads * (head_dim * elem_size(dtype) / 16) + 255) / 256
                                   : ((num_tokens + group - 1) / group * num_kv_heads + 1) / 2;
@@ -1149,12 +1151,11 @@ pa_status rows_int4(void* key, void* value, void* k_cache, void* v_cache, const 
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// Threads of a token's thread block: few tokens take 256, so that each is
-// done sooner; many take 64, which wait for one another less and set up less
-// (6166 tokens of 48 rows, normed: 256 threads 52.5 us, 128 43.0, 64 42.4).
-#ifndef PA_ROPE_MANY
-#define PA_ROPE_MANY 64
-#endif
+// Threads of a token's thread block: few tokens take 256, so that each is done
+// sooner; many (8 an SM and more) take 64, which set up less and wait for one
+// another less (6166 tokens of 48 rows, normed: 64 threads 37 us, 128 44, 32 43).
+constexpr int kRopeManyThreads = 64;
+
 template <pa::Pool POOL>
 pa_status rope_and_cache(void* q_out, const void* q, const void* key, const void* value, void* k_cache, void* v_cache,
                          const float* k_scale, const float* v_scale, const int64_t* positions,
@@ -1209,7 +1210,7 @@ pa_status rope_and_cache(void* q_out, const void* q, const void* key, const void
     p.rotary_dim = rotary_dim;
     p.block_shift = block_shift(block_size);
     p.num_slots = num_blocks * static_cast<long long>(block_size);
-    const int threads = num_tokens >= 8LL * sm_count() ? PA_ROPE_MANY : pa::kRopeThreads;
+    const int threads = num_tokens >= 8LL * sm_count() ? kRopeManyThreads : pa::kRopeThreads;
     const cudaError_t e = with_rows(dtype, head_dim, [&](auto tt, auto dd) -> cudaError_t {
         using T = typename decltype(tt)::type;
         constexpr int kD = decltype(dd)::value;

@@ -48,10 +48,11 @@ namespace pa {
 
 // Query group for the fp16 product: rows scaled by 2^shift so that the largest
 // magnitude lands in [2^13, 2^14), the operands of a 16-dim step being q_d -
-// q_d+8 / 16 and q_d+8 / 16 (rounded to fp16, 2^-12 relative: at scores of
-// standard size 1e-4 of a unit, below what rounding P costs).  sums[c][e]: the
-// fp32 sum of dims 64 c .. of heads 2 (lane % 4) + e, unscaled.
-// `raw`: row r's dims 16 ks + 2c, + 1 and + 8 of them, as loaded (zero from row `group` on).
+// q_d+8 / 16 and q_d+8 / 16.  The first is rounded to fp16, 2^-12 relative: the
+// output of a 32k context is 1.67e-3 off with it, 1.63e-3 of that the rounding to
+// bf16.  sums[c][e]: the fp32 sum of dims 64 c .. of heads 2 (lane % 4) + e,
+// unscaled.  `raw`: row r's dims 16 ks + 2c, + 1 and + 8 of them, as loaded (zero
+// from row `group` on).
 template <typename T, int D>
 __device__ __forceinline__ int q_operands(uint32_t (&qa)[D / 16][2], float (&sums)[D / 64][2],
                                           const uint32_t (&raw)[D / 16][2], int lane) {
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
 
     // O^T of codes less 7.5: (d = 16 mt + r, h = 2c), (d, 2c + 1), and that of d plus 16 times that of d + 8, the same heads
     float o[D / 16][4];
-    float ps[NC][2];         // sum of P (times 2^-24) that is still to come out of o
+    float ps[NC][2];         // sum of P (times 2^-14) that is still to come out of o
     float zo[NC][2];         // sum of p * (zero + 7.5 scale), this lane's tokens
     float m_ref[2] = {0.f, 0.f}, l_run[2] = {0.f, 0.f};
     bool started = false;    // whether a token has been attended: m_ref is a score then
@@ -320,10 +321,10 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 float(&y)[4] = o[4 * ch + m];
-                y[0] = fmaf(-7.5f, ps[ch][0], y[0]);
-                y[1] = fmaf(-7.5f, ps[ch][1], y[1]);
-                y[2] = fmaf(-127.5f, ps[ch][0], y[2]);
-                y[3] = fmaf(-127.5f, ps[ch][1], y[3]);
+                y[0] = fmaf(-7.5f / 1024.f, ps[ch][0], y[0]);   // (2^-24 / 2^-14)
+                y[1] = fmaf(-7.5f / 1024.f, ps[ch][1], y[1]);
+                y[2] = fmaf(-127.5f / 1024.f, ps[ch][0], y[2]);
+                y[3] = fmaf(-127.5f / 1024.f, ps[ch][1], y[3]);
             }
             ps[ch][0] = ps[ch][1] = 0.f;
         }
@@ -469,10 +470,14 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
             uint32_t wa[4], wb[4];
             words(vbase, 0, ch, wa);
             words(vbase, 1, ch, wb);
-            // the codes' mean part: 7.5 sum of P (as rounded), the same in every row
+            // the codes' mean part: 7.5 sum of P (as rounded), the same in every row.
+            // The ones are 2^-14, a normal number: the tensor core aligns a
+            // product by its operands' exponents, so one with the subnormal 2^-24
+            // keeps ten bits less of the sum (and 7.5 times that is lost: 1.6e-3
+            // of a 32k context's output).
             float mean[4];
-            mma_f16(mean, 0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u, pb[0], ps[ch][0], ps[ch][1], 0.f, 0.f);
-            mma_f16(mean, 0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u, pb[1], mean[0], mean[1], mean[2], mean[3]);
+            mma_f16(mean, 0x04000400u, 0x04000400u, 0x04000400u, 0x04000400u, pb[0], ps[ch][0], ps[ch][1], 0.f, 0.f);
+            mma_f16(mean, 0x04000400u, 0x04000400u, 0x04000400u, 0x04000400u, pb[1], mean[0], mean[1], mean[2], mean[3]);
             ps[ch][0] = mean[0];
             ps[ch][1] = mean[1];
 #pragma unroll

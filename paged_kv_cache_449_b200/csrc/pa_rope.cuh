@@ -44,44 +44,36 @@ struct RopeParams {
     long long num_slots;
 };
 
-#ifndef PA_ROPE_ROWS
-#define PA_ROPE_ROWS 3
-#endif
-#ifndef PA_ROPE_CTAS
-#define PA_ROPE_CTAS 4
-#endif
-constexpr int kRopeRows = PA_ROPE_ROWS;
+constexpr int kRopeRows = 3;         // rows a thread has in flight (2: 37.9 us, 4: 40.2, 3: 37.4 at 6166 tokens)
 constexpr int kRopeThreads = 256;   // at most
 
-// One CTA per token, of 64 threads (many tokens) to 256 (few); a group of D / E lanes takes one head's row at a time,
-// kRopeRows rows in flight: their loads are asked for first, then the token's
-// sines and cosines computed while they come.
+// One CTA per token, of 64 threads (many tokens) to 256 (few); a group of D / E
+// lanes takes one head's row at a time, kRopeRows rows in flight.  The rows of
+// q, k and v are three loops, so that what differs between them (the source,
+// the norm's weights, where a row goes) is set up once; the first rows are asked
+// for before the token's sines and cosines are computed.
 template <typename T, int D, Pool POOL, bool INTERLEAVED, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads, POOL == Pool::kNative ? PA_ROPE_CTAS : 3) pa_rope_cache_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, POOL == Pool::kNative ? 4 : 3) pa_rope_cache_kernel(const __grid_constant__ RopeParams p) {
     wait_for_prior_work();
     constexpr int E = Vec<T>::E, V = D / E;
-    const int step = blockDim.x / V;         // rows the CTA takes at once
     __shared__ float2 turn[D / 2];            // m cos, m sin
     const long long i = blockIdx.x;
-    const long long slot = p.slot_mapping[i];
-    const int vec = threadIdx.x % V, lane = threadIdx.x & 31;
-    const int rows = p.num_q_heads + 2 * p.num_kv_heads, v_row = p.num_q_heads + p.num_kv_heads;
+    const int vec = threadIdx.x % V, lane = threadIdx.x & 31, first = threadIdx.x / V;
+    const int step = blockDim.x / V;          // rows the CTA takes at once
     const int half = p.rotary_dim / 2;
-    const bool live = slot >= 0 && slot < p.num_slots;
-
+    const T* qsrc = reinterpret_cast<const T*>(p.q) + i * p.q_stride + vec * E;
+    const T* ksrc = reinterpret_cast<const T*>(p.key) + i * p.k_stride + vec * E;
+    const T* vsrc = reinterpret_cast<const T*>(p.value) + i * p.v_stride + vec * E;
     uint4 raw[kRopeRows];
-    auto load = [&](int r0) {
+    auto load = [&](const T* src, int heads, int base) {   // rows base + first, + step, ..
 #pragma unroll
         for (int k = 0; k < kRopeRows; ++k) {
-            const int row = r0 + k * step;
-            const T* src = reinterpret_cast<const T*>(p.q) + i * p.q_stride + row * D;
-            if (row >= p.num_q_heads) src = reinterpret_cast<const T*>(p.key) + i * p.k_stride + (row - p.num_q_heads) * D;
-            if (row >= v_row) src = reinterpret_cast<const T*>(p.value) + i * p.v_stride + (row - v_row) * D;
-            raw[k] = row < rows ? *reinterpret_cast<const uint4*>(src + vec * E) : make_uint4(0u, 0u, 0u, 0u);
+            const int h = base + k * step + first;
+            raw[k] = h < heads ? *reinterpret_cast<const uint4*>(src + h * D) : make_uint4(0u, 0u, 0u, 0u);
         }
     };
-    const int first = threadIdx.x / V;
-    load(first);
+    load(qsrc, p.num_q_heads, 0);
+    const long long slot = p.slot_mapping[i];
     for (int j = threadIdx.x; j < half; j += blockDim.x) {
         const double turns =
             static_cast<double>(p.positions[i]) * (static_cast<double>(p.inv_freq[j]) * 0.15915494309189533577);
@@ -90,10 +82,11 @@ __global__ void __launch_bounds__(kRopeThreads, POOL == Pool::kNative ? PA_ROPE_
         sincospif(2.f * part, &s, &c);
         turn[j] = make_float2(c * p.rope_scale, s * p.rope_scale);
     }
+    const bool live = slot >= 0 && slot < p.num_slots;
     if (slot >= p.num_slots && threadIdx.x == 0) flag_error(4 /* PA_DEVERR_SLOT */);
     const int block_size = 1 << p.block_shift;
-    const long long block = live ? slot >> p.block_shift : 0;
     const int t = live ? static_cast<int>(slot) & (block_size - 1) : 0;
+    const long long tile0 = (live ? slot >> p.block_shift : 0) * p.num_kv_heads;
     __syncthreads();
     // This thread's dims are the same in every row, and so are its angles.
     // Half layout: x' = x cos + y sin', y the pair's other element, which lies
@@ -111,69 +104,91 @@ __global__ void __launch_bounds__(kRopeThreads, POOL == Pool::kNative ? PA_ROPE_
             sn[e] = !INTERLEAVED && low ? -a.y : a.y;
         }
     }
-
-    // every lane of a warp takes the same number of turns: the shuffles stay whole
-    for (int r0 = first; r0 - first < rows; r0 += kRopeRows * step) {
+    // norm and rotation of one row (every lane of the warp takes part)
+    auto turn_row = [&](Vec<T>& x, const Vec<T>& g, bool norm) {
+        if (NORM && norm) {
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum = fmaf(x.f[e], x.f[e], sum);
+#pragma unroll
+            for (int off = 1; off < V; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            const float inv = rsqrtf(sum * (1.f / D) + p.eps);
+#pragma unroll
+            for (int e = 0; e < E; ++e) x.f[e] = x.f[e] * inv * g.f[e];
+        }
+        if constexpr (INTERLEAVED) {
+            if (turned) {
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const float a = x.f[e], b = x.f[e + 1];
+                    x.f[e] = a * cs[e / 2] - b * sn[e / 2];
+                    x.f[e + 1] = b * cs[e / 2] + a * sn[e / 2];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float y = __shfl_sync(0xffffffffu, x.f[e], from);
+                if (turned) x.f[e] = x.f[e] * cs[e] + y * sn[e];
+            }
+        }
+    };
+    // a row of k or v into its tile
+    auto keep = [&](Vec<T>& x, uint8_t* pool, const float* scale, int h, bool in, bool value) {
+        const bool write = in && live;
+        float scale8 = 1.f;
+        if constexpr (POOL == Pool::kE4m3) scale8 = write ? scale[h] : 1.f;
+        if constexpr (POOL != Pool::kNative) {   // (what a quantised pool holds is the rounded row's code)
+#pragma unroll
+            for (int e = 0; e < E; ++e) x.f[e] = to_float<T>(from_float<T>(x.f[e]));
+        }
+        write_row<T, D, POOL>(x, pool, write ? tile0 + h : 0, block_size, t, vec, value, scale8, write, 0xffffffffu);
+    };
+    Vec<T> g;
+    if (NORM && p.q_weight != nullptr) g.load(reinterpret_cast<const T*>(p.q_weight) + vec * E);
+    T* q_out = reinterpret_cast<T*>(p.q_out) + i * p.num_q_heads * D + vec * E;
+    for (int base = 0; base < p.num_q_heads; base += kRopeRows * step) {
+        if (base > 0) load(qsrc, p.num_q_heads, base);
 #pragma unroll
         for (int k = 0; k < kRopeRows; ++k) {
-            const int row = r0 + k * step;
-            if (row - first >= rows) break;   // (uniform)
-            const bool in = row < rows, is_q = row < p.num_q_heads, is_v = row >= v_row;
-            const int h = is_q ? row : (is_v ? row - v_row : row - p.num_q_heads);
-            const bool write = in && !is_q && live;
-            const long long tile = write ? block * p.num_kv_heads + h : 0;
-            if (POOL == Pool::kNative && __all_sync(0xffffffffu, is_v)) {   // a warp of V rows: copied as they are
-                if (write)
-                    *reinterpret_cast<uint4*>(p.v_cache + tile * block_size * D * static_cast<int>(sizeof(T)) +
-                                              (vec * block_size + t) * 16) = raw[k];
-                continue;
-            }
+            if (base + k * step >= p.num_q_heads) break;   // (uniform)
+            const int h = base + k * step + first;
             Vec<T> x;
             x.widen(raw[k]);
-            if constexpr (NORM) {
-                const T* w = reinterpret_cast<const T*>(is_q ? p.q_weight : p.k_weight);
-                float sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) sum = fmaf(x.f[e], x.f[e], sum);
-#pragma unroll
-                for (int off = 1; off < V; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                if (!is_v && w != nullptr) {
-                    const float inv = rsqrtf(sum * (1.f / D) + p.eps);
-                    Vec<T> g;
-                    g.load(w + vec * E);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) x.f[e] = x.f[e] * inv * g.f[e];
-                }
-            }
-            if constexpr (INTERLEAVED) {
-                if (turned && !is_v) {
-#pragma unroll
-                    for (int e = 0; e < E; e += 2) {
-                        const float a = x.f[e], b = x.f[e + 1];
-                        x.f[e] = a * cs[e / 2] - b * sn[e / 2];
-                        x.f[e + 1] = b * cs[e / 2] + a * sn[e / 2];
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float y = __shfl_sync(0xffffffffu, x.f[e], from);
-                    if (turned && !is_v) x.f[e] = x.f[e] * cs[e] + y * sn[e];
-                }
-            }
-            if (is_q && in)
-                *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.q_out) + (i * p.num_q_heads + h) * D + vec * E) = x.narrow();
-            if (__all_sync(0xffffffffu, is_q)) continue;
-            float scale8 = 1.f;
-            if constexpr (POOL == Pool::kE4m3) scale8 = write ? (is_v ? p.v_scale : p.k_scale)[h] : 1.f;
-            if constexpr (POOL != Pool::kNative) {   // (what a quantised pool holds is the rounded row's code)
-#pragma unroll
-                for (int e = 0; e < E; ++e) x.f[e] = to_float<T>(from_float<T>(x.f[e]));
-            }
-            write_row<T, D, POOL>(x, is_v ? p.v_cache : p.k_cache, tile, block_size, t, vec, is_v, scale8, write,
-                                  0xffffffffu);
+            turn_row(x, g, p.q_weight != nullptr);
+            if (h < p.num_q_heads) *reinterpret_cast<uint4*>(q_out + h * D) = x.narrow();
         }
-        if (r0 - first + kRopeRows * step < rows) load(r0 + kRopeRows * step);
+    }
+    if (!live) return;   // (the whole block: a token without a place keeps its q only)
+    if (NORM && p.k_weight != nullptr) g.load(reinterpret_cast<const T*>(p.k_weight) + vec * E);
+    for (int base = 0; base < p.num_kv_heads; base += kRopeRows * step) {
+        load(ksrc, p.num_kv_heads, base);
+#pragma unroll
+        for (int k = 0; k < kRopeRows; ++k) {
+            if (base + k * step >= p.num_kv_heads) break;
+            const int h = base + k * step + first;
+            Vec<T> x;
+            x.widen(raw[k]);
+            turn_row(x, g, p.k_weight != nullptr);
+            keep(x, p.k_cache, p.k_scale, h, h < p.num_kv_heads, false);
+        }
+    }
+    for (int base = 0; base < p.num_kv_heads; base += kRopeRows * step) {
+        load(vsrc, p.num_kv_heads, base);
+#pragma unroll
+        for (int k = 0; k < kRopeRows; ++k) {
+            if (base + k * step >= p.num_kv_heads) break;
+            const int h = base + k * step + first;
+            if constexpr (POOL == Pool::kNative) {   // as it is
+                if (h < p.num_kv_heads)
+                    *reinterpret_cast<uint4*>(p.v_cache + (tile0 + h) * block_size * D * static_cast<int>(sizeof(T)) +
+                                              (vec * block_size + t) * 16) = raw[k];
+            } else {
+                Vec<T> x;
+                x.widen(raw[k]);
+                keep(x, p.v_cache, p.v_scale, h, h < p.num_kv_heads, true);
+            }
+        }
     }
 }
 

@@ -91,7 +91,7 @@ def test_many_tokens_bit_for_bit(D, B, dtype):
     """Chunks that start and end anywhere in their blocks, padding, single
     tokens, a run of slots that crosses into another block's."""
     g = ou.gen(D + B)
-    H, N = 7, 64
+    H, N = 11, 64
     order = torch.randperm(N, generator=g)
     slots, used = [], 0
     for start, count in ((5, 150), (0, 97), (B - 1, 2 * B + 3), (3, 1), (0, B), (7, 100)):
@@ -102,7 +102,7 @@ def test_many_tokens_bit_for_bit(D, B, dtype):
     free = [int(b) * B + t for b in order[used:used + 3] for t in torch.randperm(B, generator=g).tolist()]
     slots = torch.tensor(slots + free)
     T = len(slots)
-    assert T * H > 2048 and used + 3 <= N
+    assert T * H > 4096 and used + 3 <= N
     k, v = ou.normal((T, H, D), dtype, g), ou.normal((T, H, D), dtype, g)
     k[:, :, 0] = torch.arange(T)[:, None] / 4.0            # quotients that are ties, or near them
     k[3], v[4] = 0.25, 0
@@ -125,7 +125,7 @@ def test_many_tokens_bit_for_bit(D, B, dtype):
 
 
 def test_a_row_that_is_not_finite_keeps_to_itself():
-    D, B, T, H = 128, 16, 1024, 3
+    D, B, T, H = 128, 16, 1024, 5
     g = ou.gen(4)
     k, v = ou.normal((T, H, D), torch.bfloat16, g), ou.normal((T, H, D), torch.bfloat16, g)
     slots = torch.arange(T)
@@ -151,8 +151,8 @@ def test_a_slot_past_the_pool_is_flagged(write):
     fn = ops.pa_reshape_and_cache_int4 if write else ops.pa_gather_cache_int4
     fn(k, k.clone(), kc, vc, torch.tensor([16, 3]).cuda())
     assert pa.pa_get_device_error() == pa.DEVERR_SLOT
-    many = torch.ones(3000, 1, 64, dtype=torch.float16).cuda()
-    slots = torch.full((3000,), -1, dtype=torch.int64)
+    many = torch.ones(5000, 1, 64, dtype=torch.float16).cuda()
+    slots = torch.full((5000,), -1, dtype=torch.int64)
     slots[100:108] = torch.arange(12, 20)      # a run that leaves the pool
     fn(many, many.clone(), kc, vc, slots.cuda())
     assert pa.pa_get_device_error() == pa.DEVERR_SLOT
