@@ -1236,7 +1236,8 @@ constexpr int kInt4Stages = 13824 / (2 * pa::int4_tile_bytes(kInt4Step, D));
 
 template <typename T, int D, int B, int NW>
 cudaError_t launch_int4(const pa::DecodeParams& p, dim3 grid, cudaStream_t stream) {
-    auto kernel = pa::pa_decode_int4_kernel<T, D, B, NW, kInt4Stages<D>>;
+    auto kernel = p.group <= 4 ? pa::pa_decode_int4_kernel<T, D, B, NW, kInt4Stages<D>, true>
+                               : pa::pa_decode_int4_kernel<T, D, B, NW, kInt4Stages<D>, false>;
     const cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel));
     if (e != cudaSuccess) return e;
     return launch_early(kernel, grid, dim3(NW * 32), pa::Int4Smem<D, B, NW, kInt4Stages<D>>::kTotal, stream,

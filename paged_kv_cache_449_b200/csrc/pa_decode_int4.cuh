@@ -34,6 +34,11 @@
 // whole tiles, issued by one lane per block, cost about a fifth of the
 // kernel's instructions.)
 //
+// Groups of up to four heads (PACK) fill only half of the product's eight
+// columns; there the second half takes the same heads for the other 16 tokens
+// of the step (the query operand of a half has zeros in the other's columns), so
+// that the softmax and all that is done per score is half the work.
+//
 // Statistics: fp32 running reference and sum in base 2.  The reference moves
 // only when a score exceeds it by 2^8 (one vote a unit instead of a reduction
 // and a rescale).  p * scale of V is rounded to fp16 for the product, within
@@ -145,7 +150,7 @@ struct Int4Smem {
     static_assert(kTile % 16 == 0, "copies move 16-byte units");
 };
 
-template <typename T, int D, int B, int NW, int ST>
+template <typename T, int D, int B, int NW, int ST, bool PACK>
 __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
     pa_decode_int4_kernel(const __grid_constant__ DecodeParams p) {
     using Sm = Int4Smem<D, B, NW, ST>;
@@ -156,6 +161,10 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
     __shared__ int last_arrival;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
+    // The tokens whose scores this lane holds: 8 h + r of the step, h < HN, from
+    // token `sub` on (PACK: the lanes of columns 4..7 hold the second 16 tokens)
+    constexpr int HN = PACK ? 2 : 4;
+    const int sub = PACK ? 16 * (c >> 1) : 0;
     const int part = blockIdx.x, kvh = blockIdx.y;
     int s = blockIdx.z;
     const uint8_t* ring = smem + warp * ST * Sm::kStage;
@@ -181,12 +190,13 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
     const int early0 = early_ids(0), early1 = early_ids(1);
     uint32_t qraw[D / 16][2];
     {
+        const int head = PACK ? r & 3 : r;
         const T* row = reinterpret_cast<const T*>(p.q) +
-                       (static_cast<long long>(s) * p.num_q_heads + kvh * group + r) * D + 2 * c;
+                       (static_cast<long long>(s) * p.num_q_heads + kvh * group + head) * D + 2 * c;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-            qraw[ks][0] = r < group ? *reinterpret_cast<const uint32_t*>(row + 16 * ks) : 0u;
-            qraw[ks][1] = r < group ? *reinterpret_cast<const uint32_t*>(row + 16 * ks + 8) : 0u;
+            qraw[ks][0] = head < group ? *reinterpret_cast<const uint32_t*>(row + 16 * ks) : 0u;
+            qraw[ks][1] = head < group ? *reinterpret_cast<const uint32_t*>(row + 16 * ks + 8) : 0u;
         }
     }
     if (L < 0 || L > p.context_cap) {
@@ -265,6 +275,17 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
     uint32_t qa[D / 16][2];
     float qsum[NC][2];
     const int shift = q_operands<T, D>(qa, qsum, qraw, lane);
+    // PACK: the query operands of the step's first 16 tokens (columns 0..3) and of its second 16 (columns 4..7)
+    uint32_t qb[PACK ? D / 16 : 1][2];
+    if constexpr (PACK) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                qb[ks][e] = r < 4 ? 0u : qa[ks][e];
+                qa[ks][e] = r < 4 ? qa[ks][e] : 0u;
+            }
+    }
     const float code_scale = ldexpf(p.score_scale, 24 - shift);
 #pragma unroll
     for (int ch = 0; ch < NC; ++ch) {
@@ -305,7 +326,8 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
         }
     };
     auto group_words = [&](const uint8_t* base, int h, uint32_t (&w)[NC]) {
-        const uint8_t* at = base + 8 * h / B * kTile + kCodes + (8 * h % B + r) * NC * 4;
+        const int t = sub + 8 * h;
+        const uint8_t* at = base + t / B * kTile + kCodes + (t % B + r) * NC * 4;
         if constexpr (NC == 2) {
             const uint2 a = *reinterpret_cast<const uint2*>(at);
             w[0] = a.x;
@@ -343,15 +365,15 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
         const int t0 = first_token(i);
         const bool whole = vis.whole(t0, 32) && !refused;
 
-        // S^T of codes, per group of dims; scores x[2h], x[2h + 1] of token 8 h + r and heads 2c, 2c + 1
+        // S^T of codes, per group of dims; scores x[2h], x[2h + 1] of this lane's token h and two heads
         // relative to the softmax's reference
-        float x[8];
+        float x[2 * HN];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        for (int h = 0; h < HN; ++h) {
             x[2 * h] = -m_ref[0];
             x[2 * h + 1] = -m_ref[1];
         }
-        float sc[2][NC][4];
+        float sc[HN / 2][NC][4];
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch) {
             uint32_t wa[4], wb[4];
@@ -359,20 +381,20 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
             words(kbase, 1, ch, wb);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const bool first = m == 0;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {   // tokens r: bytes 0 and 2; r + 8: bytes 1 and 3
+                    const bool first = m == 0 && (!PACK || g == 0);
                     const uint32_t w = g ? wb[m] : wa[m];
                     const uint32_t e = w & 0x00ff00ffu, f = __byte_perm(w, 0u, 0x4341);
-                    float(&y)[4] = sc[g][ch];
-                    mma_f16(y, e & 0x000f000fu, f & 0x000f000fu, e, f, qa[4 * ch + m],
+                    float(&y)[4] = sc[PACK ? 0 : g][ch];
+                    mma_f16(y, e & 0x000f000fu, f & 0x000f000fu, e, f, PACK && g ? qb[PACK ? 4 * ch + m : 0] : qa[4 * ch + m],
                             first ? 0.f : y[0], first ? 0.f : y[1], first ? 0.f : y[2], first ? 0.f : y[3]);
                 }
             }
         }
-        float vs[4][NC], vz[4][NC];   // V's scales, and the values of code 7.5
+        float vs[HN][NC], vz[HN][NC];   // V's scales, and the values of code 7.5
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        for (int h = 0; h < HN; ++h) {
             uint32_t kw[NC], vw[NC];
             group_words(kbase, h, kw);
             group_words(vbase, h, vw);
@@ -389,8 +411,9 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
         }
         if (!whole) {   // tokens that are not attended, or whose block id was refused: whatever lies there is not used
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                if (!(step_id(i, 8 * h / B) >= 0 && vis.token(t0 + 8 * h + r))) {
+            for (int h = 0; h < HN; ++h) {
+                const int t = sub + 8 * h;
+                if (!(step_id(i, t / B) >= 0 && vis.token(t0 + t + r))) {
                     x[2 * h] = x[2 * h + 1] = kNegInf;
 #pragma unroll
                     for (int ch = 0; ch < NC; ++ch) vs[h][ch] = vz[h][ch] = 0.f;
@@ -398,16 +421,18 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
             }
         }
         // the reference of the softmax and the unit of V's scales, moved when they have to be
-        const float mx0 = fmaxf(fmaxf(x[0], x[2]), fmaxf(x[4], x[6])), mx1 = fmaxf(fmaxf(x[1], x[3]), fmaxf(x[5], x[7]));
-        float sm = 0.f;
+        float mx0 = x[0], mx1 = x[1], sm = 0.f;
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
+        for (int h = 0; h < HN; ++h) {
+            mx0 = fmaxf(mx0, x[2 * h]);
+            mx1 = fmaxf(mx1, x[2 * h + 1]);
 #pragma unroll
             for (int ch = 0; ch < NC; ++ch) sm = fmaxf(sm, vs[h][ch]);
+        }
         if (__any_sync(0xffffffffu, mx0 > 8.f || mx1 > 8.f || sm > v_most) || !started) {
             float n0 = mx0, n1 = mx1;   // by how much the references rise
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
+            for (int off = PACK ? 2 : 4; off < 32; off <<= 1) {
                 n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
                 n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
             }
@@ -422,7 +447,7 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
             m_ref[0] += n0;
             m_ref[1] += n1;
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
+            for (int h = 0; h < HN; ++h) {
                 x[2 * h] -= n0;
                 x[2 * h + 1] -= n1;
             }
@@ -454,14 +479,15 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
             l_run[1] *= a1;
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = exp2_approx(x[e]);   // x becomes p
-        l_run[0] += (x[0] + x[2]) + (x[4] + x[6]);
-        l_run[1] += (x[1] + x[3]) + (x[5] + x[7]);
+        for (int e = 0; e < 2 * HN; ++e) {   // x becomes p
+            x[e] = exp2_approx(x[e]);
+            l_run[e & 1] += x[e];
+        }
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch) {
             uint32_t pb[2][2];   // P^T as the B operand, tokens 16 g + 8 e ..
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
+            for (int h = 0; h < HN; ++h) {
                 zo[ch][0] = fmaf(x[2 * h], vz[h][ch], zo[ch][0]);
                 zo[ch][1] = fmaf(x[2 * h + 1], vz[h][ch], zo[ch][1]);
                 const float sv = vs[h][ch] * v_unit;
@@ -477,7 +503,15 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
             // of a 32k context's output).
             float mean[4];
             mma_f16(mean, 0x04000400u, 0x04000400u, 0x04000400u, 0x04000400u, pb[0], ps[ch][0], ps[ch][1], 0.f, 0.f);
-            mma_f16(mean, 0x04000400u, 0x04000400u, 0x04000400u, 0x04000400u, pb[1], mean[0], mean[1], mean[2], mean[3]);
+            if constexpr (PACK) {   // (both halves of the step in one product) then each half's columns alone
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    pb[1][e] = r < 4 ? 0u : pb[0][e];
+                    pb[0][e] = r < 4 ? pb[0][e] : 0u;
+                }
+            } else {
+                mma_f16(mean, 0x04000400u, 0x04000400u, 0x04000400u, 0x04000400u, pb[1], mean[0], mean[1], mean[2], mean[3]);
+            }
             ps[ch][0] = mean[0];
             ps[ch][1] = mean[1];
 #pragma unroll
@@ -502,13 +536,19 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
     __syncthreads();   // (the ring is free now)
 
     // ---- this warp's state in true units, then the warps' merge
+    if constexpr (PACK) {   // the two halves of the steps
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[mt][e] += __shfl_xor_sync(0xffffffffu, o[mt][e], 2);
+    }
     float* mo = reinterpret_cast<float*>(smem);
     float* mml = mo + NW * kMaxGroup * kMergeRow<D>;
     const float back = v_unit > 0.f ? 16777216.f / v_unit : 0.f;   // 2^24 / unit
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
+        for (int off = PACK ? 2 : 4; off < 32; off <<= 1) {
             l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], off);
 #pragma unroll
             for (int ch = 0; ch < NC; ++ch) zo[ch][e] += __shfl_xor_sync(0xffffffffu, zo[ch][e], off);
