@@ -167,9 +167,9 @@ NCU_TRAFFIC = {
 
 
 # the sources each recorded kernel is compiled from (its launch configuration
-# lives in pa_api.cu)
-DECODE_SOURCES = ("pa_api.cu", "pa_decode.cuh", "pa_e4m3.cuh", "pa_warp.cuh", "pa_device.cuh", "pa_reshape.cuh")
-PREFILL_SOURCES = ("pa_api.cu", "pa_prefill_tc.cuh", "pa_prefill.cuh", "pa_device.cuh")
+# lives in pa_api.cu and pa_host.cuh)
+DECODE_SOURCES = ("pa_api.cu", "pa_host.cuh", "pa_decode.cuh", "pa_e4m3.cuh", "pa_warp.cuh", "pa_device.cuh", "pa_reshape.cuh")
+PREFILL_SOURCES = ("pa_api.cu", "pa_host.cuh", "pa_prefill_tc.cuh", "pa_prefill.cuh", "pa_device.cuh")
 # the shared-prefix step runs both kernels
 SHARED_PREFIX_SOURCES = tuple(sorted(set(DECODE_SOURCES + PREFILL_SOURCES)))
 

@@ -1,7 +1,8 @@
 """Builds libpa.so in-tree with nvcc for sm_100a (B200).
 
-The library is one translation unit (csrc/pa_api.cu plus its headers), linked
-against the static CUDA runtime so it loads without a GPU or driver present.
+The library is two translation units (csrc/pa_api.cu and csrc/pa_ops.cu plus
+their headers), compiled side by side and linked against the static CUDA runtime
+so it loads without a GPU or driver present.
 """
 
 from __future__ import annotations
@@ -13,7 +14,7 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRC = os.path.join(HERE, "csrc", "pa_api.cu")
+UNITS = [os.path.join(HERE, "csrc", name) for name in ("pa_api.cu", "pa_ops.cu")]
 LIB = os.path.join(HERE, "libpa.so")
 # The same sources with the test hooks of include/pa_test.h compiled in (for
 # the tests of the kernels' bounded waits); never loaded by the product.
@@ -29,7 +30,7 @@ def nvcc_path() -> str:
 
 
 def sources() -> list[str]:
-    return [SRC] + sorted(glob.glob(os.path.join(HERE, "csrc", "*.cuh"))) + \
+    return UNITS + sorted(glob.glob(os.path.join(HERE, "csrc", "*.cuh"))) + \
         sorted(glob.glob(os.path.join(ROOT, "include", "**", "*.h"), recursive=True))
 
 
@@ -39,15 +40,23 @@ def build(out: str = LIB, defines: dict | None = None, force: bool = False, verb
     if not force and os.path.exists(out):
         if os.path.getmtime(out) >= max(os.path.getmtime(s) for s in sources()):
             return out
-    cmd = [nvcc_path(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
-           "-shared", "-cudart", "static", "-I", os.path.join(ROOT, "include")]
-    for k, v in (defines or {}).items():
-        cmd.append(f"-D{k}={v}")
+    flags = [*ARCH, "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
+    flags += [f"-D{k}={v}" for k, v in (defines or {}).items()]
     if verbose:
-        cmd += ["-Xptxas", "-v"]
+        flags += ["-Xptxas", "-v"]
     tmp = f"{out}.tmp{os.getpid()}"
-    cmd += ["-o", tmp, SRC]
-    subprocess.run(cmd, check=True)
+    objects = [f"{tmp}.{i}.o" for i in range(len(UNITS))]
+    try:
+        running = [subprocess.Popen([nvcc_path(), *flags, "-c", "-o", obj, src]) for src, obj in zip(UNITS, objects)]
+        codes = [p.wait() for p in running]   # (every one is waited for, whatever the others did)
+        for p, code in zip(running, codes):
+            if code != 0:
+                raise subprocess.CalledProcessError(code, p.args)
+        subprocess.run([nvcc_path(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objects], check=True)
+    finally:
+        for obj in objects:
+            if os.path.exists(obj):
+                os.remove(obj)
     os.replace(tmp, out)
     return out
 

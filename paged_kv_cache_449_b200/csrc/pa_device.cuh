@@ -11,8 +11,8 @@
 
 namespace pa {
 
-// Device error word (one per GPU that loads the library).  Bits are the
-// PA_DEVERR_* values of pa.h.
+// Device error word (one per GPU that loads the library, and per translation
+// unit: pa_get_device_error joins them).  Bits are the PA_DEVERR_* values of pa.h.
 __device__ int g_device_error;
 
 __device__ __forceinline__ void flag_error(int bit) { atomicOr(&g_device_error, bit); }
