@@ -51,16 +51,16 @@
 
 namespace pa {
 
-// Query group for the fp16 product: rows scaled by 2^shift so that the largest
-// magnitude lands in [2^13, 2^14), the operands of a 16-dim step being q_d -
-// q_d+8 / 16 and q_d+8 / 16.  The first is rounded to fp16, 2^-12 relative: the
-// output of a 32k context is 1.67e-3 off with it, 1.63e-3 of that the rounding to
-// bf16.  sums[c][e]: the fp32 sum of dims 64 c .. of heads 2 (lane % 4) + e,
-// unscaled.  `raw`: row r's dims 16 ks + 2c, + 1 and + 8 of them, as loaded (zero
-// from row `group` on).
+// Query group for the fp16 product: each head's row scaled by a 2^shift of its own
+// so that its largest magnitude lands in [2^13, 2^14) (up to |q| = 2^114), the
+// operands of a 16-dim step being q_d - q_d+8 / 16 and q_d+8 / 16.  The first is
+// rounded to fp16, 2^-12 relative: the output of a 32k context is 1.67e-3 off with
+// it, 1.63e-3 of that the rounding to bf16.  Of heads 2 (lane % 4) + e: sums[c][e]
+// the fp32 sum of dims 64 c .., unscaled, shift[e] the scaling.  `raw`: row r's
+// dims 16 ks + 2c, + 1 and + 8 of them, as loaded (zero from row `group` on).
 template <typename T, int D>
-__device__ __forceinline__ int q_operands(uint32_t (&qa)[D / 16][2], float (&sums)[D / 64][2],
-                                          const uint32_t (&raw)[D / 16][2], int lane) {
+__device__ __forceinline__ void q_operands(uint32_t (&qa)[D / 16][2], float (&sums)[D / 64][2], int (&shift)[2],
+                                           const uint32_t (&raw)[D / 16][2], int lane) {
     const int c = lane & 3;
     float f[D / 16][4];
     float mx = 0.f;
@@ -76,12 +76,13 @@ __device__ __forceinline__ int q_operands(uint32_t (&qa)[D / 16][2], float (&sum
         for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(f[ks][e]));
     }
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    for (int off = 1; off < 4; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));   // (of row r)
     // floor(log2(mx)) from the exponent field (a subnormal bf16 maximum counts as 2^-127)
     const int e2 = mx > 0.f ? static_cast<int>((__float_as_uint(mx) >> 23) & 0xff) - 127 : 13;
-    int shift = 13 - e2;
-    shift = shift > 100 ? 100 : (shift < -100 ? -100 : shift);
-    const float mul = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);   // 2^shift
+    const int row_shift = 13 - e2 > 100 ? 100 : (13 - e2 < -100 ? -100 : 13 - e2);
+    const float mul = __uint_as_float(static_cast<uint32_t>(127 + row_shift) << 23);   // 2^shift
+    shift[0] = __shfl_sync(0xffffffffu, row_shift, 8 * c);
+    shift[1] = __shfl_sync(0xffffffffu, row_shift, 8 * c + 4);
 #pragma unroll
     for (int ch = 0; ch < D / 64; ++ch) {
         float sum = 0.f;
@@ -101,7 +102,6 @@ __device__ __forceinline__ int q_operands(uint32_t (&qa)[D / 16][2], float (&sum
         sums[ch][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
         sums[ch][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
     }
-    return shift;
 }
 
 // D(16x8 f32) = A(16x16 fp16) B(16x8 fp16) + C; not volatile: the compiler may
@@ -134,7 +134,7 @@ struct VisibleSteps {
     __device__ __forceinline__ bool any(int t, int n) const { return t < L && (wlo - t < n || t < sinks); }
 };
 
-// Warps an SM holds.  D = 128: 12 of 157 registers (one pass over 64 sequences
+// Warps an SM holds.  D = 128: 12 of 160 registers (one pass over 64 sequences
 // 30.6 us, the 70B long batch 142 us) rather than 16 of 128 (32.7 and 150 us).
 template <int D>
 constexpr int kInt4Resident = D == 128 ? 12 : 16;
@@ -274,7 +274,8 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
 
     uint32_t qa[D / 16][2];
     float qsum[NC][2];
-    const int shift = q_operands<T, D>(qa, qsum, qraw, lane);
+    int shift[2];
+    q_operands<T, D>(qa, qsum, shift, qraw, lane);
     // PACK: the query operands of the step's first 16 tokens (columns 0..3) and of its second 16 (columns 4..7)
     uint32_t qb[PACK ? D / 16 : 1][2];
     if constexpr (PACK) {
@@ -286,12 +287,12 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
                 qa[ks][e] = r < 4 ? qa[ks][e] : 0u;
             }
     }
-    const float code_scale = ldexpf(p.score_scale, 24 - shift);
+    // scores are score_scale 2^(24 - shift) times scale * (the product with codes) + zero * (the sum of q 2^(shift - 24))
+    const float code_scale[2] = {ldexpf(p.score_scale, 24 - shift[0]), ldexpf(p.score_scale, 24 - shift[1])};
 #pragma unroll
-    for (int ch = 0; ch < NC; ++ch) {
-        qsum[ch][0] *= p.score_scale;
-        qsum[ch][1] *= p.score_scale;
-    }
+    for (int ch = 0; ch < NC; ++ch)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) qsum[ch][e] = ldexpf(qsum[ch][e], shift[e] - 24);
 
     // O^T of codes less 7.5: (d = 16 mt + r, h = 2c), (d, 2c + 1), and that of d plus 16 times that of d + 8, the same heads
     float o[D / 16][4];
@@ -369,10 +370,7 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
         // relative to the softmax's reference
         float x[2 * HN];
 #pragma unroll
-        for (int h = 0; h < HN; ++h) {
-            x[2 * h] = -m_ref[0];
-            x[2 * h + 1] = -m_ref[1];
-        }
+        for (int e = 0; e < 2 * HN; ++e) x[e] = 0.f;
         float sc[HN / 2][NC][4];
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch) {
@@ -400,7 +398,7 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
             group_words(vbase, h, vw);
 #pragma unroll
             for (int ch = 0; ch < NC; ++ch) {
-                const float ks = __uint_as_float(kw[ch] << 16) * code_scale;
+                const float ks = __uint_as_float(kw[ch] << 16);
                 const float kz = __uint_as_float(kw[ch] & 0xffff0000u);
                 const float(&q)[4] = sc[h / 2][ch];
                 x[2 * h] = fmaf(ks, q[2 * (h & 1)], fmaf(kz, qsum[ch][0], x[2 * h]));
@@ -408,6 +406,8 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
                 vs[h][ch] = __uint_as_float(vw[ch] << 16);
                 vz[h][ch] = fmaf(7.5f, vs[h][ch], __uint_as_float(vw[ch] & 0xffff0000u));
             }
+            x[2 * h] = fmaf(x[2 * h], code_scale[0], -m_ref[0]);
+            x[2 * h + 1] = fmaf(x[2 * h + 1], code_scale[1], -m_ref[1]);
         }
         if (!whole) {   // tokens that are not attended, or whose block id was refused: whatever lies there is not used
 #pragma unroll
@@ -436,6 +436,13 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
                 n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
                 n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
             }
+            if (sm == INFINITY) {   // a group that is not finite: its output is not, and the unit is the others'
+                sm = 0.f;
+#pragma unroll
+                for (int h = 0; h < HN; ++h)
+#pragma unroll
+                    for (int ch = 0; ch < NC; ++ch) sm = vs[h][ch] < INFINITY ? fmaxf(sm, vs[h][ch]) : sm;
+            }
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) sm = fmaxf(sm, __shfl_xor_sync(0xffffffffu, sm, off));
             const bool any = __any_sync(0xffffffffu, n0 != kNegInf);   // (a step masks all heads alike)
@@ -452,7 +459,7 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
                 x[2 * h + 1] -= n1;
             }
             float vu = 1.f;
-            if (sm > v_most) {   // (scales are bf16: below 2^128; an infinite one makes the output NaN)
+            if (sm > v_most) {   // (scales are bf16: below 2^128)
                 const int e = static_cast<int>((__float_as_uint(sm) >> 23) & 0xff) - 127;   // sm < 2^(e + 1)
                 int up = 5 - e;                                                             // p * scale <= 2^8 2^7
                 up = up > 126 ? 126 : up;
@@ -544,7 +551,8 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
     }
     float* mo = reinterpret_cast<float*>(smem);
     float* mml = mo + NW * kMaxGroup * kMergeRow<D>;
-    const float back = v_unit > 0.f ? 16777216.f / v_unit : 0.f;   // 2^24 / unit
+    // 2^24 / unit, in two factors: the quotient is infinite for units below 2^-104
+    const float back = v_unit > 0.f ? 1.f / v_unit : 0.f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -558,8 +566,8 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
             float* row = mo + (warp * kMaxGroup + h) * kMergeRow<D>;
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt) {
-                row[16 * mt + r] = fmaf(o[mt][e], back, zo[mt / 4][e]);
-                row[16 * mt + 8 + r] = fmaf(o[mt][2 + e] - o[mt][e], back * 0.0625f, zo[mt / 4][e]);
+                row[16 * mt + r] = fmaf(o[mt][e] * 16777216.f, back, zo[mt / 4][e]);
+                row[16 * mt + 8 + r] = fmaf((o[mt][2 + e] - o[mt][e]) * 1048576.f, back, zo[mt / 4][e]);
             }
             if (r == 0) {
                 mml[(warp * kMaxGroup + h) * 2] = started ? m_ref[e] : kNegInf;

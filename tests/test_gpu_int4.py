@@ -305,3 +305,58 @@ def test_blocks_of_byte_pools_are_copied():
     table[0, 1] = free[0]
     kc[old], vc[old] = 0xff, 0xff
     assert torch.equal(run(q, kc, vc, table, lens), base)
+
+
+def row_errors(got, want):
+    return ((got.double().cpu() - want).norm(dim=-1) / want.norm(dim=-1))
+
+
+@pytest.mark.parametrize("big", [float("inf"), float("nan"), 2.0 ** 40])
+@pytest.mark.parametrize("group", [2, 4, 8])
+def test_a_head_of_another_size_keeps_to_itself(group, big):
+    lens = [200, 33]
+    q, kc, vc, table, rows = build(lens, 2 * group, 2, 128, 16, torch.bfloat16, group)
+    want = ou.decode(q, rows, lens, 128 ** -0.5)
+    q[:, 1] *= big
+    q[:, group + 1, 5] = big
+    others = [h for h in range(2 * group) if h % group != 1]
+    for part in (0, 64):
+        got = run(q, kc, vc, table, lens, partition_size=part)
+        assert float(row_errors(got, want)[:, others].max()) <= BOUND[torch.bfloat16]
+        if big != 2.0 ** 40:
+            assert not torch.isfinite(got[:, 1]).any()
+
+
+@pytest.mark.parametrize("group", [2, 8])
+@pytest.mark.parametrize("bad", ["inf", "nan", "span"])
+def test_a_group_of_v_that_is_not_finite_keeps_to_its_dims(bad, group):
+    """One token's first 64 dims of V: the other dims' output stays what it is."""
+    L, D, B = 150, 128, 16
+    g = ou.gen(31)
+    k, v = (ou.normal((L, 1, D), torch.float32, g) for _ in range(2))
+    q = ou.normal((1, group, D), torch.bfloat16, g)
+    want = ou.attend(q, ou.values4(k), ou.values4(v), L - 1, D ** -0.5, 0, 0)[..., 64:]
+    v[77, 0, 3] = 3e38 if bad == "span" else float(bad)
+    v[77, 0, 9] = -3e38 if bad == "span" else 1.0
+    N = -(-L // B)
+    kc, vc = (x.cuda() for x in empty_pools(N, 1, D, B))
+    ops.pa_reshape_and_cache_int4(k.cuda(), v.cuda(), kc, vc, torch.arange(L).cuda())
+    for part in (0, 32):
+        got = run(q, kc, vc, torch.arange(N, dtype=torch.int32).reshape(1, -1), [L], partition_size=part)
+        assert not torch.isfinite(got[..., :64]).any()
+        assert float(row_errors(got[..., 64:], want).max()) <= BOUND[torch.bfloat16]
+
+
+@pytest.mark.parametrize("size", [2.0 ** 116, 2.0 ** -116])
+def test_values_of_far_sizes(size):
+    L, D, B = 150, 64, 16
+    g = ou.gen(32)
+    k, v = (ou.normal((L, 1, D), torch.float32, g) for _ in range(2))
+    v = v.bfloat16().float() * size
+    q = ou.normal((1, 4, D), torch.bfloat16, g)
+    N = -(-L // B)
+    kc, vc = (x.cuda() for x in empty_pools(N, 1, D, B))
+    ops.pa_reshape_and_cache_int4(k.cuda(), v.cuda(), kc, vc, torch.arange(L).cuda())
+    want = ou.attend(q, ou.values4(k), ou.values4(v), L - 1, D ** -0.5, 0, 0)
+    got = run(q, kc, vc, torch.arange(N, dtype=torch.int32).reshape(1, -1), [L])
+    assert float(row_errors(got, want).max()) <= BOUND[torch.bfloat16]
