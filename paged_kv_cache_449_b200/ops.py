@@ -164,6 +164,14 @@ def pa_rope_and_cache_int4(q_out, q, key, value, k_cache, v_cache, positions, sl
     _check(load().pa_rope_and_cache_int4(*args, _stream(stream)), "pa_rope_and_cache_int4")
 
 
+def _settled(args, keep):
+    """A prepared call may run on any stream: counters that were made (zeroed)
+    for it on the current one are complete before it exists."""
+    if keep and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(keep[0].device).synchronize()
+    return args, keep
+
+
 def _prepared(name, args, tensors) -> Prepared:
     dev = _tensor_device(tensors, {})
     if dev is None:
@@ -329,8 +337,9 @@ def prepare_decode_int4(out, q, k_cache, v_cache, block_tables, context_lens, sc
     """pa_decode_int4's arguments checked and marshalled once (see Prepared);
     the object has its own workspace and counters where none are given, so two
     of its calls must not overlap."""
-    args, keep = _decode_int4_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
-                                   window, num_sinks, partition_size, workspace, counters, seq_order)
+    args, keep = _settled(*_decode_int4_args(out, q, k_cache, v_cache, block_tables, context_lens, scale,
+                                             max_context_len, window, num_sinks, partition_size, workspace,
+                                             counters, seq_order))
     return _prepared("pa_decode_int4", args, (out, q, k_cache, v_cache, block_tables, context_lens, seq_order, *keep))
 
 
@@ -393,9 +402,9 @@ def prepare_decode_window(out, q, key, value, k_cache, v_cache, block_tables, co
     """pa_decode_window's arguments (pa_decode_window_fp8's where scales are
     given) checked and marshalled once (see Prepared); its own workspace and
     counters as in prepare_decode_int4."""
-    args, keep = _decode_window_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables,
-                                     context_lens, scale, window, num_sinks, max_context_len, partition_size,
-                                     workspace, counters, seq_order, ref_counts)
+    args, keep = _settled(*_decode_window_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables,
+                                               context_lens, scale, window, num_sinks, max_context_len,
+                                               partition_size, workspace, counters, seq_order, ref_counts))
     return _prepared("pa_decode_window" + ("" if k_scale is None else "_fp8"), args,
                      (out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, seq_order,
                       ref_counts, *keep))

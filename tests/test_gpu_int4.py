@@ -360,3 +360,23 @@ def test_values_of_far_sizes(size):
     want = ou.attend(q, ou.values4(k), ou.values4(v), L - 1, D ** -0.5, 0, 0)
     got = run(q, kc, vc, torch.arange(N, dtype=torch.int32).reshape(1, -1), [L])
     assert float(row_errors(got, want).max()) <= BOUND[torch.bfloat16]
+
+
+def test_prepared_calls_on_a_stream_of_their_own():
+    """The handle's counters are zero before any stream uses them."""
+    lens = [3000] * 2
+    q, kc, vc, table, rows = build(lens, 8, 1, 64, 16, torch.bfloat16, 14)
+    base = run(q, kc, vc, table, lens, partition_size=64)
+    lens_d, table_d, qd = torch.tensor(lens, dtype=torch.int32).cuda(), table.cuda(), q.cuda()
+    side = torch.cuda.Stream()
+    out = torch.zeros_like(base)
+    torch.cuda.synchronize()
+    busy = torch.randn(4096, 4096, device="cuda")
+    for _ in range(8):
+        busy = busy @ busy * 1e-3
+        call = pa.prepare_decode_int4(out, qd, kc, vc, table_d, lens_d, 0.125, partition_size=64)
+        call(side)
+        side.synchronize()
+        assert torch.equal(out, base)
+        out.zero_()
+        torch.cuda.synchronize()
