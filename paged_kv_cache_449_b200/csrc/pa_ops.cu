@@ -469,8 +469,9 @@ pa_status pa_prefill_window(void* out, const void* q, const void* k_cache, const
     p.context_cap = context_cap(sh);
     p.num_blocks = num_blocks;
     p.tile_tokens = 128 / p.group;
-    p.window = window;
-    p.num_sinks = num_sinks;
+    // (no more than the context: the kernel's differences of positions stay within 32 bits)
+    p.window = std::min(window, std::max(1, p.context_cap));
+    p.num_sinks = std::min(num_sinks, p.context_cap);
     const long long per_cta = static_cast<long long>(prefill_tiles_per_cta(block_size, false)) * p.tile_tokens;
     const long long tiles = (static_cast<long long>(max_query_len) + per_cta - 1) / per_cta;
     if (tiles > INT_MAX) return PA_ERR_UNSUPPORTED;
