@@ -76,9 +76,9 @@ pa_status pa_rope_and_cache_int4(void* q_out, const void* q, const void* key, co
  *     scale = (maximum - zero) / 15 rounded up to bf16 (0 if that is 0, else at least 2^-126)
  *     code  = (x - zero) / scale rounded to the nearest whole number, ties to even, in 0..15 (0 where scale is 0)
  *     value = zero + scale * code
- * every step in fp32.  A group that is
- * not finite, or whose span is not, reads back as values that are not finite.  Pools are byte arrays of (block, kv head) tiles of
- * block_size * head_dim * 9 / 16 bytes:
+ * every step in fp32.  A group that is not finite, or whose span is not, reads
+ * back as values that are not finite.  Pools are byte arrays of (block, kv head)
+ * tiles of block_size * head_dim * 9 / 16 bytes:
  *   codes   block_size * head_dim / 2 bytes.  A byte holds dims d (low nibble)
  *           and d + 8 of one token, d % 16 < 8.  With u = token % 8,
  *           chunk = d / 64, m = d % 64 / 16, e = d % 8:
@@ -111,8 +111,8 @@ pa_status pa_gather_cache_int4(void* key, void* value, const void* k_cache, cons
  * Sliding window with first tokens that stay visible (sinks).  The query at
  * position p attends to the tokens t <= p with t > p - window or t <
  * num_sinks.  Blocks that hold no such token are not read, and their
- * block-table entries may hold anything; the others' tokens that are not
- * visible do not count, whatever the pool holds there.
+ * block-table entries may hold anything; the others' tokens that no query of the
+ * sequence sees do not count, whatever the pool holds there.
  *
  * The decode entries below share a plan:
  *   partition_size  0: one thread block per (sequence, kv head); otherwise the
@@ -174,8 +174,9 @@ pa_status pa_decode_int4(void* out, const void* q, const void* k_cache, const vo
 
 /*
  * pa_prefill_window — pa_prefill with a sliding window (window >= 1, num_sinks
- * >= 0) for every query; scale must be positive.  Other arguments and errors as
- * in pa_prefill.  There is no form without a tensor map: PA_ERR_UNSUPPORTED
+ * >= 0) for every query; scale must be positive.  A token that some query of the
+ * chunk attends to has to be finite: otherwise it may reach the others, as in
+ * pa_prefill.  Other arguments and errors as in pa_prefill.  There is no form without a tensor map: PA_ERR_UNSUPPORTED
  * where 16- or 32-token blocks would need one that cannot be built.
  */
 pa_status pa_prefill_window(void* out, const void* q, const void* k_cache, const void* v_cache,

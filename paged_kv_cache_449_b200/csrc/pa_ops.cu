@@ -345,7 +345,8 @@ pa_status pa_decode_int4_plan(int num_seqs, int num_q_heads, int num_kv_heads, i
         max_context_len < 0 || *partition_size < -1 || check_window(window, num_sinks, 0) != PA_OK)
         return PA_ERR_INVALID_ARG;
     const long long units = visible_units(max_context_len, window, num_sinks, kInt4Step);
-    if (*partition_size < 0) *partition_size = choose_int4_partition(static_cast<long long>(num_seqs) * num_kv_heads, units, kInt4Step);
+    if (*partition_size < 0)
+        *partition_size = choose_int4_partition(static_cast<long long>(num_seqs) * num_kv_heads, units, kInt4Step);
     if (*partition_size % kInt4Step != 0) return PA_ERR_INVALID_ARG;
     const long long parts = window_partitions(units, kInt4Step, *partition_size);
     *bytes = parts > 1 ? splitk_bytes(num_seqs, num_q_heads, parts, head_dim) : 0;

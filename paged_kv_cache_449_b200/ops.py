@@ -194,7 +194,7 @@ def prepare_rope_and_cache(q_out, q, key, value, k_cache, v_cache, positions, sl
 
 
 # ---- 4-bit pools: uint8 tensors [num_blocks, Hkv, block_size * head_dim * 9 // 16] (one tile of codes and group
-#      words per (block, head); its byte order is that of pa.h)
+#      words per (block, head); its byte order is that of pa/ops.h)
 
 def int4_pool_shape(num_blocks, num_kv_heads, head_dim, block_size):
     return (num_blocks, num_kv_heads, block_size * head_dim * 9 // 16)
