@@ -163,7 +163,8 @@ pa_status pa_decode_window_fp8(void* out, const void* q, const void* key, const 
  * bf16; PA_ERR_UNSUPPORTED for fp32), whole (window 0) or with a sliding
  * window.  The codes are multiplied as whole numbers, scales and zeros applied
  * in fp32; each head's query (|q| < 2^114) is scaled by a power of two into
- * fp16 range first and rounded there.
+ * fp16's range first, exactly (elements below 2^-23 of the head's largest keep
+ * 2^-34 of it).
  */
 pa_status pa_decode_int4(void* out, const void* q, const void* k_cache, const void* v_cache,
                          const int32_t* block_tables, const int32_t* context_lens, float scale, int block_size,

@@ -11,14 +11,16 @@
 // the scales and zeros cost a few fp32 operations a token and head.
 //
 // A byte holds the codes a and b of two dims (d and d + 8).  Put at the bottom
-// of an fp16 pattern it is the subnormal (a + 16 b) 2^-24, and its low four
-// bits are a 2^-24; the tensor cores multiply subnormals exactly.  So two ANDs
-// (or a byte permute and an AND) make the operands a and a + 16 b of both
-// bytes of a register, and the mixture is taken apart where that is free: for K,
-// whose two dims lie along the product's sum, in the query,
-//     a q_d + b q_d+8 = a (q_d - q_d+8 / 16) + (a + 16 b) (q_d+8 / 16),
-// for V, whose two dims are rows of the output, by one subtraction at the end.
-// A word of a tile is a whole operand of one MMA in four operations.
+// of an fp16 pattern its low four bits are the subnormal a 2^-24, its high four
+// 16 b 2^-24, the whole byte (a + 16 b) 2^-24; the tensor cores multiply
+// subnormals exactly.  For K the two dims lie along the product's sum: the
+// operands are a and 16 b (an AND each, a shift for the upper bytes of the two
+// halves), and the sixteenth goes into the query, where it is exact.  For V they
+// are rows of the output: the operands are a and a + 16 b, taken
+// apart by one subtraction at the end.  (The same for K would take the query
+// operand q_d - q_d+8 / 16, which has to be rounded to fp16: outputs were up to
+// 5.6e-3 (fp16) and 1.1e-2 (bf16) off for queries of size 32, for one operation
+// less in each of the step's 16 words of K, 3% of its instructions.)
 //
 // Codes are taken about their middle, value = (zero + 7.5 scale) + scale (code
 // - 7.5): over many tokens of like weight sum p scale code and sum p zero
@@ -53,9 +55,9 @@ namespace pa {
 
 // Query group for the fp16 product: each head's row scaled by a 2^shift of its own
 // so that its largest magnitude lands in [2^13, 2^14) (up to |q| = 2^114), the
-// operands of a 16-dim step being q_d - q_d+8 / 16 and q_d+8 / 16.  The first is
-// rounded to fp16, 2^-12 relative: the output of a 32k context is 1.67e-3 off with
-// it, 1.63e-3 of that the rounding to bf16.  Of heads 2 (lane % 4) + e: sums[c][e]
+// operands of a 16-dim step being q_d and q_d+8 / 16.  Both are exact (fp16 and
+// bf16 elements have 11 and 8 bits), but for elements below 2^-23 of the row's
+// largest, which keep 2^-34 of it.  Of heads 2 (lane % 4) + e: sums[c][e]
 // the fp32 sum of dims 64 c .., unscaled, shift[e] the scaling.  `raw`: row r's
 // dims 16 ks + 2c, + 1 and + 8 of them, as loaded (zero from row `group` on).
 template <typename T, int D>
@@ -90,10 +92,8 @@ __device__ __forceinline__ void q_operands(uint32_t (&qa)[D / 16][2], float (&su
         for (int m = 0; m < 4; ++m) {
             const float(&x)[4] = f[4 * ch + m];
             sum += (x[0] + x[1]) + (x[2] + x[3]);
-            // the operand pairs are (code, code + 16 code of the dim 8 on): see the kernel
-            const float b0 = x[2] * mul * 0.0625f, b1 = x[3] * mul * 0.0625f;
-            const __half2 a = __floats2half2_rn(x[0] * mul - b0, x[1] * mul - b1);
-            const __half2 b = __floats2half2_rn(b0, b1);
+            const __half2 a = __floats2half2_rn(x[0] * mul, x[1] * mul);
+            const __half2 b = __floats2half2_rn(x[2] * mul * 0.0625f, x[3] * mul * 0.0625f);
             qa[4 * ch + m][0] = *reinterpret_cast<const uint32_t*>(&a);
             qa[4 * ch + m][1] = *reinterpret_cast<const uint32_t*>(&b);
         }
@@ -383,9 +383,9 @@ __global__ void __launch_bounds__(NW * 32, kInt4Resident<D> / NW)
                 for (int g = 0; g < 2; ++g) {   // tokens r: bytes 0 and 2; r + 8: bytes 1 and 3
                     const bool first = m == 0 && (!PACK || g == 0);
                     const uint32_t w = g ? wb[m] : wa[m];
-                    const uint32_t e = w & 0x00ff00ffu, f = __byte_perm(w, 0u, 0x4341);
+                    const uint32_t f = w >> 8;
                     float(&y)[4] = sc[PACK ? 0 : g][ch];
-                    mma_f16(y, e & 0x000f000fu, f & 0x000f000fu, e, f, PACK && g ? qb[PACK ? 4 * ch + m : 0] : qa[4 * ch + m],
+                    mma_f16(y, w & 0x000f000fu, f & 0x000f000fu, w & 0x00f000f0u, f & 0x00f000f0u, PACK && g ? qb[PACK ? 4 * ch + m : 0] : qa[4 * ch + m],
                             first ? 0.f : y[0], first ? 0.f : y[1], first ? 0.f : y[2], first ? 0.f : y[3]);
                 }
             }
