@@ -319,13 +319,20 @@ def pa_decode_int4(out, q, k_cache, v_cache, block_tables, context_lens, scale, 
     _check(load().pa_decode_int4(*args, _side_stream(stream, keep)), "pa_decode_int4")
 
 
+def _stream_object(raw, device):
+    """The torch stream of a raw handle.  Handles 0 and 1 both name the legacy
+    default stream; ExternalStream takes a null handle as none given and returns
+    a stream of torch's pool."""
+    return torch.cuda.default_stream(device) if raw in (0, 1) else torch.cuda.ExternalStream(raw, device=device)
+
+
 def _side_stream(stream, keep):
     """The call's raw stream; buffers that were made on the current stream and
     are used on another are kept from reuse until that one has passed here."""
     raw = _stream(stream)
     current = torch.cuda.current_stream()
     if raw != current.cuda_stream and keep:
-        side = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw)
+        side = stream if isinstance(stream, torch.cuda.Stream) else _stream_object(raw, keep[0].device)
         side.wait_stream(current)   # (their allocation, and the counters' zeroing, lie on the current stream)
         for t in keep:
             t.record_stream(side)

@@ -1,0 +1,75 @@
+"""Which streams a call's own buffers are ordered and kept on (CPU: the streams
+and tensors are stand-ins that note what is asked of them)."""
+
+import pytest
+import torch
+
+import paged_kv_cache_449_b200 as pa
+from paged_kv_cache_449_b200 import ops
+
+
+class Stream:
+    def __init__(self, raw):
+        self.cuda_stream, self.waits = raw, []
+        self.device = torch.device("cuda", 0)
+
+    def wait_stream(self, other):
+        self.waits.append(other)
+
+
+class Buffer:
+    """A tensor made for a call."""
+
+    def __init__(self):
+        self.device, self.recorded = torch.device("cuda", 0), []
+
+    def record_stream(self, stream):
+        self.recorded.append(stream)
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """The legacy default stream, and a stream of the caller's that is current;
+    raw handles are opened as torch does: handle 0 means "none given", and gives
+    a stream of the pool."""
+    default, current, pool = Stream(0), Stream(0x1000), Stream(0x9000)
+    made = {}
+
+    def external(raw, device=None):
+        return made.setdefault(raw, Stream(raw)) if raw else pool
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: default)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", external)
+    monkeypatch.setattr(pa, "_stream", lambda stream: current.cuda_stream if stream is None else
+                        getattr(stream, "cuda_stream", stream))
+    monkeypatch.setattr(ops, "_stream", pa._stream)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    return default, current, made
+
+
+@pytest.mark.parametrize("handle", [0, 1])
+def test_the_default_streams_handle_is_that_stream(streams, handle):
+    """Handles 0 and 1 both name the legacy default stream."""
+    default, current, made = streams
+    buffer = Buffer()
+    assert ops._side_stream(handle, (buffer,)) == handle
+    assert buffer.recorded == [default] and default.waits == [current] and not made
+
+
+def test_a_raw_handle_and_a_stream_object(streams):
+    default, current, made = streams
+    buffer = Buffer()
+    assert ops._side_stream(0x2000, (buffer,)) == 0x2000
+    assert buffer.recorded == [made[0x2000]] and made[0x2000].waits == [current]
+    mine = Stream(0x3000)
+    assert ops._side_stream(mine, (buffer,)) == 0x3000
+    assert buffer.recorded[1:] == [mine] and mine.waits == [current]
+
+
+def test_the_current_stream_needs_neither(streams):
+    default, current, made = streams
+    buffer = Buffer()
+    for stream in (None, current, current.cuda_stream):
+        assert ops._side_stream(stream, (buffer,)) == current.cuda_stream
+    assert not buffer.recorded and not current.waits
