@@ -164,12 +164,13 @@ def pa_rope_and_cache_int4(q_out, q, key, value, k_cache, v_cache, positions, sl
     _check(load().pa_rope_and_cache_int4(*args, _stream(stream)), "pa_rope_and_cache_int4")
 
 
-def _settled(args, keep):
+def _settled(args, held, made):
     """A prepared call may run on any stream: counters that were made (zeroed)
-    for it on the current one are complete before it exists."""
-    if keep and not torch.cuda.is_current_stream_capturing():
-        torch.cuda.current_stream(keep[0].device).synchronize()
-    return args, keep
+    for it on the current one are complete before it exists.  (Buffers of the
+    caller's are the caller's to order, and are not waited for.)"""
+    if made and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(made[0].device).synchronize()
+    return args, held
 
 
 def _prepared(name, args, tensors) -> Prepared:
@@ -262,20 +263,28 @@ def pa_decode_int4_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, max_conte
 
 
 def _partials(need, workspace, counters, num_counters, device):
-    """[pointer, bytes, pointer, count] of a call's workspace and counters, and
-    the tensors: made here where None, for this call alone (calls that overlap
-    may not share them)."""
+    """[pointer, bytes, pointer, count] of a call's workspace and counters, the
+    two tensors, and those of them that were made here because they were not
+    given, for this call alone (calls that overlap may not share them)."""
     if need == 0:
-        return [None, 0, None, 0], ()
+        return [None, 0, None, 0], (), ()
+    made = ()
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        made += (workspace,)
     if counters is None:
         counters = torch.zeros(num_counters, dtype=torch.int32, device=device)
-    buf = counters.get(num_counters, device) if isinstance(counters, Counters) else counters
+        made += (counters,)
+    buf = counters
+    if isinstance(counters, Counters):
+        had = counters.buf
+        buf = counters.get(num_counters, device)
+        if buf is not had:
+            made += (buf,)
     if buf.dtype != torch.int32:
         raise ValueError("counters must be int32")
     return [_dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-            _dev_ptr(buf, "counters"), buf.numel()], (workspace, buf)
+            _dev_ptr(buf, "counters"), buf.numel()], (workspace, buf), made
 
 
 def _batch(out, q, block_tables, context_lens):
@@ -299,11 +308,11 @@ def _decode_int4_args(out, q, k_cache, v_cache, block_tables, context_lens, scal
         max_context_len = int(block_tables.shape[1]) * b
     cap = min(int(max_context_len), int(block_tables.shape[1]) * b)
     part, need = pa_decode_int4_plan(S, Hq, hkv, D, cap, window, num_sinks, partition_size)
-    extra, tensors = _partials(need, workspace, counters, S * hkv, q.device)
+    extra, held, made = _partials(need, workspace, counters, S * hkv, q.device)
     return [_dev_ptr(out, "out"), _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
             _dev_ptr(block_tables, "block_tables"), _dev_ptr(context_lens, "context_lens"), float(scale), b, S, Hq,
             hkv, D, int(block_tables.shape[1]), int(max_context_len), k_cache.shape[0], _DTYPE[q.dtype], int(window),
-            int(num_sinks), part, *extra, _order_ptr(seq_order, S)], tensors
+            int(num_sinks), part, *extra, _order_ptr(seq_order, S)], held, made
 
 
 @_on_tensor_device
@@ -314,9 +323,9 @@ def pa_decode_int4(out, q, k_cache, v_cache, block_tables, context_lens, scale, 
     partition of the context (0: one; None: the library's choice); workspace
     and counters (zeroed int32 [S * Hkv], left at zero) as pa_decode_int4_plan
     says, made here for this call where None."""
-    args, keep = _decode_int4_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
-                                   window, num_sinks, partition_size, workspace, counters, seq_order)
-    _check(load().pa_decode_int4(*args, _side_stream(stream, keep)), "pa_decode_int4")
+    args, held, _ = _decode_int4_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
+                                      window, num_sinks, partition_size, workspace, counters, seq_order)
+    _check(load().pa_decode_int4(*args, _side_stream(stream, held)), "pa_decode_int4")
 
 
 def _stream_object(raw, device):
@@ -326,15 +335,16 @@ def _stream_object(raw, device):
     return torch.cuda.default_stream(device) if raw in (0, 1) else torch.cuda.ExternalStream(raw, device=device)
 
 
-def _side_stream(stream, keep):
-    """The call's raw stream; buffers that were made on the current stream and
-    are used on another are kept from reuse until that one has passed here."""
+def _side_stream(stream, held):
+    """The call's raw stream; a workspace and counters that lie on the current
+    stream (made there for this call, as a rule) and are used on another are
+    ordered before the call and kept from reuse until that one has passed here."""
     raw = _stream(stream)
     current = torch.cuda.current_stream()
-    if raw != current.cuda_stream and keep:
-        side = stream if isinstance(stream, torch.cuda.Stream) else _stream_object(raw, keep[0].device)
+    if raw != current.cuda_stream and held:
+        side = stream if isinstance(stream, torch.cuda.Stream) else _stream_object(raw, held[0].device)
         side.wait_stream(current)   # (their allocation, and the counters' zeroing, lie on the current stream)
-        for t in keep:
+        for t in held:
             t.record_stream(side)
     return raw
 
@@ -344,10 +354,10 @@ def prepare_decode_int4(out, q, k_cache, v_cache, block_tables, context_lens, sc
     """pa_decode_int4's arguments checked and marshalled once (see Prepared);
     the object has its own workspace and counters where none are given, so two
     of its calls must not overlap."""
-    args, keep = _settled(*_decode_int4_args(out, q, k_cache, v_cache, block_tables, context_lens, scale,
+    args, held = _settled(*_decode_int4_args(out, q, k_cache, v_cache, block_tables, context_lens, scale,
                                              max_context_len, window, num_sinks, partition_size, workspace,
                                              counters, seq_order))
-    return _prepared("pa_decode_int4", args, (out, q, k_cache, v_cache, block_tables, context_lens, seq_order, *keep))
+    return _prepared("pa_decode_int4", args, (out, q, k_cache, v_cache, block_tables, context_lens, seq_order, *held))
 
 
 def _decode_window_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
@@ -371,10 +381,10 @@ def _decode_window_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale, 
                          max_context_len)
     cap = min(args[-3], int(block_tables.shape[1]) * b)
     part, need = pa_decode_window_plan(S, Hq, hkv, D, b, cap, window, num_sinks, partition_size)
-    extra, tensors = _partials(need, workspace, counters, S * hkv, q.device)
+    extra, held, made = _partials(need, workspace, counters, S * hkv, q.device)
     return [args[0], args[1], None if key is None else _dev_ptr(key, "key"),
             None if value is None else _dev_ptr(value, "value"), *args[2:], int(window), int(num_sinks), part, *extra,
-            _counts_ptr(ref_counts, n), _order_ptr(seq_order, S)], tensors
+            _counts_ptr(ref_counts, n), _order_ptr(seq_order, S)], held, made
 
 
 @_on_tensor_device
@@ -386,10 +396,10 @@ def pa_decode_window(out, q, key, value, k_cache, v_cache, block_tables, context
     tokens and the first num_sinks.  Blocks outside may have left the block
     table.  partition_size, workspace, counters as in pa_decode_int4 (see
     pa_decode_window_plan)."""
-    args, keep = _decode_window_args(out, q, key, value, k_cache, v_cache, None, None, block_tables, context_lens,
-                                     scale, window, num_sinks, max_context_len, partition_size, workspace, counters,
-                                     seq_order, ref_counts)
-    _check(load().pa_decode_window(*args, _side_stream(stream, keep)), "pa_decode_window")
+    args, held, _ = _decode_window_args(out, q, key, value, k_cache, v_cache, None, None, block_tables, context_lens,
+                                        scale, window, num_sinks, max_context_len, partition_size, workspace, counters,
+                                        seq_order, ref_counts)
+    _check(load().pa_decode_window(*args, _side_stream(stream, held)), "pa_decode_window")
 
 
 @_on_tensor_device
@@ -397,10 +407,10 @@ def pa_decode_window_fp8(out, q, key, value, k_cache, v_cache, k_scale, v_scale,
                          window, num_sinks=0, max_context_len=None, partition_size=None, workspace=None,
                          counters=None, stream=None, seq_order=None, ref_counts=None):
     """pa_decode_window over 8-bit pools."""
-    args, keep = _decode_window_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables,
-                                     context_lens, scale, window, num_sinks, max_context_len, partition_size,
-                                     workspace, counters, seq_order, ref_counts)
-    _check(load().pa_decode_window_fp8(*args, _side_stream(stream, keep)), "pa_decode_window_fp8")
+    args, held, _ = _decode_window_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables,
+                                        context_lens, scale, window, num_sinks, max_context_len, partition_size,
+                                        workspace, counters, seq_order, ref_counts)
+    _check(load().pa_decode_window_fp8(*args, _side_stream(stream, held)), "pa_decode_window_fp8")
 
 
 def prepare_decode_window(out, q, key, value, k_cache, v_cache, block_tables, context_lens, scale, window,
@@ -409,12 +419,12 @@ def prepare_decode_window(out, q, key, value, k_cache, v_cache, block_tables, co
     """pa_decode_window's arguments (pa_decode_window_fp8's where scales are
     given) checked and marshalled once (see Prepared); its own workspace and
     counters as in prepare_decode_int4."""
-    args, keep = _settled(*_decode_window_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables,
+    args, held = _settled(*_decode_window_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables,
                                                context_lens, scale, window, num_sinks, max_context_len,
                                                partition_size, workspace, counters, seq_order, ref_counts))
     return _prepared("pa_decode_window" + ("" if k_scale is None else "_fp8"), args,
                      (out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, seq_order,
-                      ref_counts, *keep))
+                      ref_counts, *held))
 
 
 def _prefill_window_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start, scale, window, num_sinks,

@@ -66,3 +66,20 @@ def test_a_call_on_another_stream(setting, kind, which):
     assert all(torch.equal(o, base[kind]) for o in outs)
     assert pa.pa_get_device_error() == 0
     del side
+
+
+@pytest.mark.parametrize("kind", ["int4", "window"])
+def test_a_handle_over_the_callers_buffers_is_made_at_once(setting, kind):
+    calls, base = setting
+    _, prepare, args, kw = calls[kind]
+    done = torch.cuda.Event()
+    out = torch.zeros_like(base[kind])
+    workspace, counters = torch.empty(1 << 20, dtype=torch.uint8, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20 * BUSY)
+    done.record()
+    call = prepare(*args(out), partition_size=64, workspace=workspace, counters=counters, **kw)
+    at_once = not done.query()
+    call()
+    torch.cuda.synchronize()
+    assert at_once and torch.equal(out, base[kind])

@@ -73,3 +73,40 @@ def test_the_current_stream_needs_neither(streams):
     for stream in (None, current, current.cuda_stream):
         assert ops._side_stream(stream, (buffer,)) == current.cuda_stream
     assert not buffer.recorded and not current.waits
+
+
+class Held(torch.Tensor):
+    """A CPU tensor that passes for one of the caller's CUDA buffers."""
+
+    @staticmethod
+    def of(t):
+        return torch.Tensor._make_subclass(Held, t)
+
+    @property
+    def is_cuda(self):
+        return True
+
+
+def test_only_buffers_made_for_a_handle_are_waited_for(monkeypatch):
+    """A prepared call waits, on the host, for the counters made for it, and for
+    nothing where the workspace and counters are the caller's."""
+    waited = []
+
+    class Busy:
+        def synchronize(self):
+            waited.append(self)
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Busy())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    workspace, counts = Held.of(torch.zeros(256, dtype=torch.uint8)), Held.of(torch.zeros(8, dtype=torch.int32))
+    kept = pa.Counters()
+    kept.buf, kept.get = counts, lambda n, device: counts
+    for counters in (counts, kept):
+        got = ops._partials(256, workspace, counters, 8, torch.device("cuda", 0))
+        assert got[0] == [workspace.data_ptr(), 256, counts.data_ptr(), 8]
+        args, held = ops._settled(*got)
+        assert held[0] is workspace and held[1] is counts and not waited
+    assert ops._settled(*ops._partials(0, None, None, 8, torch.device("cuda", 0))) == ([None, 0, None, 0], ())
+    made = torch.zeros(8, dtype=torch.int32)
+    ops._settled([], (workspace, made), (made,))
+    assert len(waited) == 1
