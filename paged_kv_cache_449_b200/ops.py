@@ -167,7 +167,8 @@ def pa_rope_and_cache_int4(q_out, q, key, value, k_cache, v_cache, positions, sl
 def _settled(args, held, made):
     """A prepared call may run on any stream: counters that were made (zeroed)
     for it on the current one are complete before it exists.  (Buffers of the
-    caller's are the caller's to order, and are not waited for.)"""
+    caller's are the caller's to order, and are not waited for; a capturing
+    stream has made no counters, see _partials.)"""
     if made and not torch.cuda.is_current_stream_capturing():
         torch.cuda.current_stream(made[0].device).synchronize()
     return args, held
@@ -262,13 +263,23 @@ def pa_decode_int4_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, max_conte
     return int(part.value), int(size.value)
 
 
-def _partials(need, workspace, counters, num_counters, device):
+def _partials(need, workspace, counters, num_counters, device, lasting):
     """[pointer, bytes, pointer, count] of a call's workspace and counters, the
     two tensors, and those of them that were made here because they were not
-    given, for this call alone (calls that overlap may not share them)."""
+    given, for this call alone (calls that overlap may not share them).
+    `lasting`: they outlive this call.  What a capture makes is zeroed by the
+    graph's replays, not now, so counters that outlive the captured call (a
+    handle's, a Counters') are not made while the stream is capturing."""
     if need == 0:
         return [None, 0, None, 0], (), ()
     made = ()
+    if isinstance(counters, Counters):
+        missing = counters.buf is None or counters.buf.numel() < num_counters or counters.buf.device != device
+    else:
+        missing = counters is None and lasting
+    if missing and torch.cuda.is_current_stream_capturing():
+        raise ValueError("counters that outlive the call cannot be made while the stream is capturing: prepare the "
+                         "call before the capture, or give zeroed counters")
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
         made += (workspace,)
@@ -298,7 +309,7 @@ def _batch(out, q, block_tables, context_lens):
 
 
 def _decode_int4_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len, window, num_sinks,
-                      partition_size, workspace, counters, seq_order):
+                      partition_size, workspace, counters, seq_order, lasting=False):
     _batch(out, q, block_tables, context_lens)
     S, Hq, D = q.shape
     if block_tables.shape[0] != S:
@@ -308,7 +319,7 @@ def _decode_int4_args(out, q, k_cache, v_cache, block_tables, context_lens, scal
         max_context_len = int(block_tables.shape[1]) * b
     cap = min(int(max_context_len), int(block_tables.shape[1]) * b)
     part, need = pa_decode_int4_plan(S, Hq, hkv, D, cap, window, num_sinks, partition_size)
-    extra, held, made = _partials(need, workspace, counters, S * hkv, q.device)
+    extra, held, made = _partials(need, workspace, counters, S * hkv, q.device, lasting)
     return [_dev_ptr(out, "out"), _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
             _dev_ptr(block_tables, "block_tables"), _dev_ptr(context_lens, "context_lens"), float(scale), b, S, Hq,
             hkv, D, int(block_tables.shape[1]), int(max_context_len), k_cache.shape[0], _DTYPE[q.dtype], int(window),
@@ -353,16 +364,17 @@ def prepare_decode_int4(out, q, k_cache, v_cache, block_tables, context_lens, sc
                         num_sinks=0, partition_size=None, workspace=None, counters=None, seq_order=None) -> Prepared:
     """pa_decode_int4's arguments checked and marshalled once (see Prepared);
     the object has its own workspace and counters where none are given, so two
-    of its calls must not overlap."""
+    of its calls must not overlap, and it is not made while the stream is
+    capturing (captured calls of it are fine)."""
     args, held = _settled(*_decode_int4_args(out, q, k_cache, v_cache, block_tables, context_lens, scale,
                                              max_context_len, window, num_sinks, partition_size, workspace,
-                                             counters, seq_order))
+                                             counters, seq_order, lasting=True))
     return _prepared("pa_decode_int4", args, (out, q, k_cache, v_cache, block_tables, context_lens, seq_order, *held))
 
 
 def _decode_window_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
                         window, num_sinks, max_context_len, partition_size, workspace, counters, seq_order,
-                        ref_counts):
+                        ref_counts, lasting=False):
     _batch(out, q, block_tables, context_lens)
     if (key is None) != (value is None):
         raise ValueError("key and value go together (both None: no append)")
@@ -381,7 +393,7 @@ def _decode_window_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale, 
                          max_context_len)
     cap = min(args[-3], int(block_tables.shape[1]) * b)
     part, need = pa_decode_window_plan(S, Hq, hkv, D, b, cap, window, num_sinks, partition_size)
-    extra, held, made = _partials(need, workspace, counters, S * hkv, q.device)
+    extra, held, made = _partials(need, workspace, counters, S * hkv, q.device, lasting)
     return [args[0], args[1], None if key is None else _dev_ptr(key, "key"),
             None if value is None else _dev_ptr(value, "value"), *args[2:], int(window), int(num_sinks), part, *extra,
             _counts_ptr(ref_counts, n), _order_ptr(seq_order, S)], held, made
@@ -421,7 +433,8 @@ def prepare_decode_window(out, q, key, value, k_cache, v_cache, block_tables, co
     counters as in prepare_decode_int4."""
     args, held = _settled(*_decode_window_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables,
                                                context_lens, scale, window, num_sinks, max_context_len,
-                                               partition_size, workspace, counters, seq_order, ref_counts))
+                                               partition_size, workspace, counters, seq_order, ref_counts,
+                                               lasting=True))
     return _prepared("pa_decode_window" + ("" if k_scale is None else "_fp8"), args,
                      (out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, seq_order,
                       ref_counts, *held))

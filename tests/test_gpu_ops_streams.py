@@ -83,3 +83,34 @@ def test_a_handle_over_the_callers_buffers_is_made_at_once(setting, kind):
     call()
     torch.cuda.synchronize()
     assert at_once and torch.equal(out, base[kind])
+
+
+@pytest.mark.parametrize("kind", ["int4", "window"])
+def test_a_handle_is_not_made_in_a_capture(setting, kind):
+    """... where it would have counters that only the graph zeroes; with the
+    caller's, or made before, its captured calls are the eager ones."""
+    calls, base = setting
+    fn, prepare, args, kw = calls[kind]
+    outs = [torch.zeros_like(base[kind]) for _ in range(3)]
+    counters = torch.zeros(2, dtype=torch.int32, device="cuda")
+    before = prepare(*args(outs[0]), partition_size=64, **kw)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError, match="capturing"):
+            prepare(*args(outs[0]), partition_size=64, **kw)
+        with pytest.raises(ValueError, match="capturing"):
+            fn(*args(outs[0]), partition_size=64, counters=pa.Counters(), **kw)
+        before()
+        given = prepare(*args(outs[1]), partition_size=64, counters=counters, **kw)
+        given()
+        fn(*args(outs[2]), partition_size=64, **kw)     # buffers of its own, in the graph
+    given()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[1], base[kind])
+    for _ in range(2):
+        for out in outs:
+            out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, base[kind]) for o in outs)
+    assert pa.pa_get_device_error() == 0

@@ -102,11 +102,32 @@ def test_only_buffers_made_for_a_handle_are_waited_for(monkeypatch):
     kept = pa.Counters()
     kept.buf, kept.get = counts, lambda n, device: counts
     for counters in (counts, kept):
-        got = ops._partials(256, workspace, counters, 8, torch.device("cuda", 0))
+        got = ops._partials(256, workspace, counters, 8, torch.device("cpu"), True)
         assert got[0] == [workspace.data_ptr(), 256, counts.data_ptr(), 8]
         args, held = ops._settled(*got)
         assert held[0] is workspace and held[1] is counts and not waited
-    assert ops._settled(*ops._partials(0, None, None, 8, torch.device("cuda", 0))) == ([None, 0, None, 0], ())
+    assert ops._settled(*ops._partials(0, None, None, 8, torch.device("cpu"), True)) == ([None, 0, None, 0], ())
     made = torch.zeros(8, dtype=torch.int32)
     ops._settled([], (workspace, made), (made,))
     assert len(waited) == 1
+
+
+def test_counters_that_outlive_a_captured_call_are_not_made_in_the_capture(monkeypatch):
+    """They would be zeroed by the graph's replays only."""
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    cpu, workspace = torch.device("cpu"), Held.of(torch.zeros(256, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="capturing"):
+        ops._partials(256, workspace, None, 8, cpu, True)
+    small = pa.Counters()
+    for lasting in (True, False):
+        for buf in (None, Held.of(torch.zeros(7, dtype=torch.int32))):
+            small.buf = buf
+            with pytest.raises(ValueError, match="capturing"):
+                ops._partials(256, workspace, small, 8, cpu, lasting)
+    assert small.buf.numel() == 7
+    # given, large enough, or not needed
+    given = Held.of(torch.zeros(8, dtype=torch.int32))
+    small.buf, small.get = given, lambda n, device: given
+    for counters in (given, small):
+        assert ops._partials(256, workspace, counters, 8, cpu, True)[1][1] is given
+    assert ops._partials(0, None, None, 8, cpu, True)[1] == ()
