@@ -150,6 +150,13 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _stream_object(raw, device):
+    """The torch stream of a raw handle.  Handles 0 and 1 both name the legacy
+    default stream; ExternalStream takes a null handle as none given and returns
+    a stream of torch's pool."""
+    return torch.cuda.default_stream(device) if raw in (0, 1) else torch.cuda.ExternalStream(raw, device=device)
+
+
 def _check(status: int, what: str):
     if status != 0:
         raise PagedAttentionError(status, what)
@@ -299,9 +306,12 @@ class Prepared:
     that holds its tensors.  For a step repeated over fixed buffers, as a
     serving loop does, it spares the per-call argument work; the buffers'
     contents may change between calls, their storage may not (the object keeps
-    a reference to each tensor)."""
+    a reference to each tensor, and has to live as long as a graph that holds
+    its calls).  `made`: those tensors that were made for it; they are kept from
+    reuse until every stream that it was called on has passed its calls (so
+    those streams have to live as long as it does)."""
 
-    def __init__(self, name, args, device, tensors):
+    def __init__(self, name, args, device, tensors, made=()):
         self._fn = getattr(load(), name)
         self._name = name
         # each argument already of its ctypes type, so a call converts nothing
@@ -310,12 +320,19 @@ class Prepared:
         self._args = tuple(a if isinstance(a, t) else t(a) for a, t in zip(args, types))
         self._device = device.index
         self._tensors = tensors
+        self._made, self._streams = made, set()
 
     def __call__(self, stream=None):
         if torch.cuda.current_device() != self._device:
             with torch.cuda.device(self._device):
                 return self(stream)
-        _check(self._fn(*self._args, _stream(stream)), self._name)
+        raw = _stream(stream)
+        if self._made and raw not in self._streams:
+            side = stream if isinstance(stream, torch.cuda.Stream) else _stream_object(raw, self._made[0].device)
+            for t in self._made:
+                t.record_stream(side)   # (nothing where they were made on that stream)
+            self._streams.add(raw)
+        _check(self._fn(*self._args, raw), self._name)
 
 
 def prepare_decode_append(out, q, key, value, k_cache, v_cache, block_tables, context_lens, scale,
@@ -384,10 +401,9 @@ def prepare_decode_shared_prefix(out, q, key, value, k_cache, v_cache, block_tab
     dev = _tensor_device(tensors + ((counters,) if isinstance(counters, torch.Tensor) else ()), {})
     if dev is None:
         raise ValueError("pa_decode_shared_prefix takes CUDA tensors")
-    args, workspace, buf = _shared_prefix_args(out, q, key, value, k_cache, v_cache, block_tables, context_lens,
-                                               scale, prefix_blocks, max_context_len, workspace, ref_counts,
-                                               counters)
-    return Prepared("pa_decode_shared_prefix", args, dev, tensors + (workspace, buf))
+    args, used, buf = _shared_prefix_args(out, q, key, value, k_cache, v_cache, block_tables, context_lens, scale,
+                                          prefix_blocks, max_context_len, workspace, ref_counts, counters)
+    return Prepared("pa_decode_shared_prefix", args, dev, tensors + (used, buf), (used,) if workspace is None else ())
 
 
 def pa_decode_splitk_workspace_size(num_seqs, num_q_heads, head_dim, max_context_len, partition_size=512) -> int:

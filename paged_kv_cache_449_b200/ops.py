@@ -15,7 +15,7 @@ import math
 import torch
 
 from . import (_DTYPE, Counters, Prepared, _check, _counts_ptr, _decode_args, _dev_ptr, _fp8_args, _on_tensor_device,
-               _order_ptr, _pool_dims, _scale_ptr, _stream, _tensor_device, load)
+               _order_ptr, _pool_dims, _scale_ptr, _stream, _stream_object, _tensor_device, load)
 
 __all__ = ["pa_rope_and_cache", "pa_rope_and_cache_fp8", "pa_rope_and_cache_int4", "prepare_rope_and_cache",
            "rope_frequencies", "int4_pool_shape", "pa_reshape_and_cache_int4", "prepare_reshape_and_cache_int4",
@@ -171,14 +171,14 @@ def _settled(args, held, made):
     stream has made no counters, see _partials.)"""
     if made and not torch.cuda.is_current_stream_capturing():
         torch.cuda.current_stream(made[0].device).synchronize()
-    return args, held
+    return args, held, made
 
 
-def _prepared(name, args, tensors) -> Prepared:
+def _prepared(name, args, tensors, made=()) -> Prepared:
     dev = _tensor_device(tensors, {})
     if dev is None:
         raise ValueError(f"{name} takes CUDA tensors")
-    return Prepared(name, args, dev, tensors)
+    return Prepared(name, args, dev, tensors, made)
 
 
 def prepare_rope_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq,
@@ -339,13 +339,6 @@ def pa_decode_int4(out, q, k_cache, v_cache, block_tables, context_lens, scale, 
     _check(load().pa_decode_int4(*args, _side_stream(stream, held)), "pa_decode_int4")
 
 
-def _stream_object(raw, device):
-    """The torch stream of a raw handle.  Handles 0 and 1 both name the legacy
-    default stream; ExternalStream takes a null handle as none given and returns
-    a stream of torch's pool."""
-    return torch.cuda.default_stream(device) if raw in (0, 1) else torch.cuda.ExternalStream(raw, device=device)
-
-
 def _side_stream(stream, held):
     """The call's raw stream; a workspace and counters that lie on the current
     stream (made there for this call, as a rule) and are used on another are
@@ -365,11 +358,12 @@ def prepare_decode_int4(out, q, k_cache, v_cache, block_tables, context_lens, sc
     """pa_decode_int4's arguments checked and marshalled once (see Prepared);
     the object has its own workspace and counters where none are given, so two
     of its calls must not overlap, and it is not made while the stream is
-    capturing (captured calls of it are fine)."""
-    args, held = _settled(*_decode_int4_args(out, q, k_cache, v_cache, block_tables, context_lens, scale,
-                                             max_context_len, window, num_sinks, partition_size, workspace,
-                                             counters, seq_order, lasting=True))
-    return _prepared("pa_decode_int4", args, (out, q, k_cache, v_cache, block_tables, context_lens, seq_order, *held))
+    capturing (captured calls of it are fine, while it lives)."""
+    args, held, made = _settled(*_decode_int4_args(out, q, k_cache, v_cache, block_tables, context_lens, scale,
+                                                   max_context_len, window, num_sinks, partition_size, workspace,
+                                                   counters, seq_order, lasting=True))
+    return _prepared("pa_decode_int4", args, (out, q, k_cache, v_cache, block_tables, context_lens, seq_order, *held),
+                     made)
 
 
 def _decode_window_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
@@ -431,13 +425,13 @@ def prepare_decode_window(out, q, key, value, k_cache, v_cache, block_tables, co
     """pa_decode_window's arguments (pa_decode_window_fp8's where scales are
     given) checked and marshalled once (see Prepared); its own workspace and
     counters as in prepare_decode_int4."""
-    args, held = _settled(*_decode_window_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables,
-                                               context_lens, scale, window, num_sinks, max_context_len,
-                                               partition_size, workspace, counters, seq_order, ref_counts,
-                                               lasting=True))
+    args, held, made = _settled(*_decode_window_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale,
+                                                     block_tables, context_lens, scale, window, num_sinks,
+                                                     max_context_len, partition_size, workspace, counters, seq_order,
+                                                     ref_counts, lasting=True))
     return _prepared("pa_decode_window" + ("" if k_scale is None else "_fp8"), args,
                      (out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, seq_order,
-                      ref_counts, *held))
+                      ref_counts, *held), made)
 
 
 def _prefill_window_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start, scale, window, num_sinks,

@@ -114,3 +114,29 @@ def test_a_handle_is_not_made_in_a_capture(setting, kind):
         torch.cuda.synchronize()
         assert all(torch.equal(o, base[kind]) for o in outs)
     assert pa.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", ["int4", "window"])
+@pytest.mark.parametrize("which", ["default", "raw", "object"])
+def test_a_handle_may_be_dropped_while_its_call_waits(setting, kind, which):
+    """... on another stream: its workspace and counters are not given to new
+    work on the stream that they were made on."""
+    calls, base = setting
+    _, prepare, args, kw = calls[kind]
+    named, side = handles()
+    busy = torch.cuda.default_stream() if which == "default" else side
+    mine = torch.cuda.Stream()
+    for _ in range(3):
+        out = torch.zeros_like(base[kind])
+        torch.cuda.synchronize()
+        with torch.cuda.stream(mine):
+            call = prepare(*args(out), partition_size=64, **kw)
+            with torch.cuda.stream(busy):
+                torch.cuda._sleep(BUSY)
+            call(named[which])
+            del call
+            junk = [torch.full((n,), 0x7f7f7f7f, dtype=torch.int32, device="cuda") for n in (2, 2, 4, 8, 1 << 16, 1 << 17, 1 << 17)]
+        torch.cuda.synchronize()
+        assert torch.equal(out, base[kind])
+        del junk
+    assert pa.pa_get_device_error() == 0

@@ -44,6 +44,7 @@ def streams(monkeypatch):
     monkeypatch.setattr(pa, "_stream", lambda stream: current.cuda_stream if stream is None else
                         getattr(stream, "cuda_stream", stream))
     monkeypatch.setattr(ops, "_stream", pa._stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "Stream", Stream)
     return default, current, made
 
@@ -104,9 +105,10 @@ def test_only_buffers_made_for_a_handle_are_waited_for(monkeypatch):
     for counters in (counts, kept):
         got = ops._partials(256, workspace, counters, 8, torch.device("cpu"), True)
         assert got[0] == [workspace.data_ptr(), 256, counts.data_ptr(), 8]
-        args, held = ops._settled(*got)
+        args, held, made = ops._settled(*got)
+        assert made == ()
         assert held[0] is workspace and held[1] is counts and not waited
-    assert ops._settled(*ops._partials(0, None, None, 8, torch.device("cpu"), True)) == ([None, 0, None, 0], ())
+    assert ops._settled(*ops._partials(0, None, None, 8, torch.device("cpu"), True)) == ([None, 0, None, 0], (), ())
     made = torch.zeros(8, dtype=torch.int32)
     ops._settled([], (workspace, made), (made,))
     assert len(waited) == 1
@@ -131,3 +133,37 @@ def test_counters_that_outlive_a_captured_call_are_not_made_in_the_capture(monke
     for counters in (given, small):
         assert ops._partials(256, workspace, counters, 8, cpu, True)[1][1] is given
     assert ops._partials(0, None, None, 8, cpu, True)[1] == ()
+
+
+def test_a_handles_own_buffers_are_kept_on_every_stream_it_runs_on(streams, monkeypatch):
+    """A handle may be dropped while its kernel still runs on another stream than
+    the one that its workspace and counters were made on."""
+    import ctypes
+    default, current, made = streams
+    launches = []
+
+    def entry(*args):
+        launches.append(args[-1])
+        return 0
+
+    entry.argtypes = [ctypes.c_int, ctypes.c_void_p]
+    monkeypatch.setattr(pa, "load", lambda: type("Library", (), {"pa_entry": staticmethod(entry)}))
+    mine, buffers = Stream(0x4000), (Buffer(), Buffer())
+    call = pa.Prepared("pa_entry", [3], torch.device("cuda", 0), (), buffers)
+    for stream in (None, mine, 0x5000, 0, mine, None, 0x5000):
+        call(stream)
+    assert launches == [current.cuda_stream, 0x4000, 0x5000, 0, 0x4000, current.cuda_stream, 0x5000]
+    for b in buffers:
+        assert [s.cuda_stream for s in b.recorded] == [current.cuda_stream, 0x4000, 0x5000, 0]
+        assert b.recorded[1] is mine and b.recorded[3] is default
+    plain = pa.Prepared("pa_entry", [3], torch.device("cuda", 0), ())
+    plain(mine)
+    assert launches[-1] == 0x4000 and not mine.waits
+
+
+def test_the_shared_prefix_handles_workspace_is_its_own_where_none_is_given(monkeypatch):
+    own = object()
+    monkeypatch.setattr(pa, "_tensor_device", lambda *a: torch.device("cuda", 0))
+    monkeypatch.setattr(pa, "_shared_prefix_args", lambda *a: ([], a[11] if a[11] is not None else own, object()))
+    assert pa.prepare_decode_shared_prefix(*[None] * 8, 0.1, 4)._made == (own,)
+    assert pa.prepare_decode_shared_prefix(*[None] * 8, 0.1, 4, workspace=object())._made == ()
