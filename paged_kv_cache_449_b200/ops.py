@@ -372,10 +372,11 @@ def _decode_window_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale, 
     _batch(out, q, block_tables, context_lens)
     if (key is None) != (value is None):
         raise ValueError("key and value go together (both None: no append)")
-    if key is not None and (key.dtype != q.dtype or value.dtype != q.dtype):
-        raise ValueError("key and value share q's dtype")
     S, Hq, D = q.shape
     n, hkv, d, b = _pool_dims(k_cache)
+    for t, name in ((key, "key"), (value, "value")):
+        if t is not None and (t.dtype != q.dtype or t.shape != (S, hkv, D)):
+            raise ValueError(f"{name} must be [S, Hkv, D] of q's dtype")
     if d != D or v_cache.shape != k_cache.shape or block_tables.shape[0] != S:
         raise ValueError("the pools' head dim is q's, and q holds one row per sequence")
     if k_scale is None:

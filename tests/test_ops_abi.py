@@ -205,3 +205,41 @@ def test_frequencies():
             pa.rope_frequencies(R, base, **bad)
     with pytest.raises(ValueError):
         pa.rope_frequencies(15)
+
+
+class _Cuda(torch.Tensor):
+    """A CPU tensor that passes the binding's check for CUDA tensors."""
+
+    @staticmethod
+    def of(*shape, dtype=torch.bfloat16):
+        return torch.Tensor._make_subclass(_Cuda, torch.zeros(shape, dtype=dtype))
+
+    @property
+    def is_cuda(self):
+        return True
+
+
+def window_args(key, value, fp8=False):
+    """ops._decode_window_args of a batch of 3 sequences, 4 query and 2 kv heads of 64 dims."""
+    q, i32 = _Cuda.of(3, 4, 64), dict(dtype=torch.int32)
+    pool = _Cuda.of(*pa.fp8_pool_shape(5, 2, 64, 16), dtype=torch.uint8) if fp8 else \
+        _Cuda.of(*pa.pool_shape(5, 2, 64, 16, torch.bfloat16))
+    scales = [_Cuda.of(2, dtype=torch.float32)] * 2 if fp8 else [None, None]
+    return ops._decode_window_args(q, q, key, value, pool, pool, *scales, _Cuda.of(3, 7, **i32), _Cuda.of(3, **i32),
+                                   0.125, 10, 0, None, 0, None, None, None, None)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_windowed_append_takes_a_row_per_sequence(lib, fp8):
+    """Fewer rows than sequences would be read out of range."""
+    good = _Cuda.of(3, 2, 64)
+    assert window_args(good, good, fp8)[0][2:4] == [good.data_ptr()] * 2
+    assert window_args(None, None, fp8)[0][2:4] == [None, None]
+    for bad in (_Cuda.of(2, 2, 64), _Cuda.of(4, 2, 64), _Cuda.of(3, 1, 64), _Cuda.of(3, 2, 32), _Cuda.of(2, 3, 64),
+                _Cuda.of(3, 2, 64, dtype=torch.float32), _Cuda.of(3, 2, 128)[..., ::2]):
+        for key, value in ((bad, good), (good, bad), (bad, bad)):
+            with pytest.raises(ValueError):
+                window_args(key, value, fp8)
+    for key, value in ((good, None), (None, good)):
+        with pytest.raises(ValueError):
+            window_args(key, value, fp8)
