@@ -279,10 +279,18 @@ def _counts_ptr(ref_counts, num_blocks):
     return _dev_ptr(ref_counts, "ref_counts")
 
 
+def _new_row_ptr(t, q, num_kv_heads, name):
+    """The newest tokens' key or value: a row of Hkv x D elements of q's dtype for every sequence of q [S, Hq, D]."""
+    if t.dtype != q.dtype or t.numel() < q.shape[0] * num_kv_heads * q.shape[2]:
+        raise ValueError(f"{name} must be [S, Hkv, D] of q's dtype")
+    return _dev_ptr(t, name)
+
+
 def _append_args(out, q, key, value, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
                  seq_order, ref_counts):
     args = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len)
-    return [args[0], args[1], _dev_ptr(key, "key"), _dev_ptr(value, "value"), *args[2:],
+    hkv = k_cache.shape[1]
+    return [args[0], args[1], _new_row_ptr(key, q, hkv, "key"), _new_row_ptr(value, q, hkv, "value"), *args[2:],
             _counts_ptr(ref_counts, k_cache.shape[0]), _order_ptr(seq_order, q.shape[0])]
 
 
@@ -366,8 +374,8 @@ def _shared_prefix_args(out, q, key, value, k_cache, v_cache, block_tables, cont
         need = pa_decode_shared_prefix_workspace_size(S, Hq, D, prefix_blocks, b)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     args = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len)
-    kp = None if key is None else _dev_ptr(key, "key")
-    vp = None if value is None else _dev_ptr(value, "value")
+    kp = None if key is None else _new_row_ptr(key, q, k_cache.shape[1], "key")
+    vp = None if value is None else _new_row_ptr(value, q, k_cache.shape[1], "value")
     if counters is None:
         counters = _default_counters.setdefault(q.device.index, Counters())
     buf = counters.get(S * k_cache.shape[1], q.device) if isinstance(counters, Counters) else counters
@@ -575,7 +583,8 @@ def pa_decode_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, cont
 def _append_fp8_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
                      max_context_len, seq_order, ref_counts):
     args = _fp8_args(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, max_context_len)
-    return [args[0], args[1], _dev_ptr(key, "key"), _dev_ptr(value, "value"), *args[2:],
+    hkv = k_cache.shape[1]
+    return [args[0], args[1], _new_row_ptr(key, q, hkv, "key"), _new_row_ptr(value, q, hkv, "value"), *args[2:],
             _counts_ptr(ref_counts, k_cache.shape[0]), _order_ptr(seq_order, q.shape[0])]
 
 

@@ -243,3 +243,25 @@ def test_windowed_append_takes_a_row_per_sequence(lib, fp8):
     for key, value in ((good, None), (None, good)):
         with pytest.raises(ValueError):
             window_args(key, value, fp8)
+
+
+def test_append_rows_of_the_plain_decodes(lib):
+    """pa_decode_append, its 8-bit form and the shared-prefix form: at least a row
+    per sequence, of q's type (contiguous rows of any shape, as ever)."""
+    q, i32 = _Cuda.of(3, 4, 64), dict(dtype=torch.int32)
+    tables, lens, scales = _Cuda.of(3, 7, **i32), _Cuda.of(3, **i32), [_Cuda.of(2, dtype=torch.float32)] * 2
+    pool = _Cuda.of(*pa.pool_shape(5, 2, 64, 16, torch.bfloat16))
+    pool8 = _Cuda.of(*pa.fp8_pool_shape(5, 2, 64, 16), dtype=torch.uint8)
+    work, counts = _Cuda.of(1 << 20, dtype=torch.uint8), _Cuda.of(6, **i32)
+    forms = [lambda k, v: pa._append_args(q, q, k, v, pool, pool, tables, lens, 0.125, None, None, None),
+             lambda k, v: pa._append_fp8_args(q, q, k, v, pool8, pool8, *scales, tables, lens, 0.125, None, None, None),
+             lambda k, v: pa._shared_prefix_args(q, q, k, v, pool, pool, tables, lens, 0.125, 1, None, work, None, counts)[0]]
+    good = _Cuda.of(3, 2, 64)
+    for form in forms:
+        for ok in (good, _Cuda.of(3, 128), _Cuda.of(5, 2, 64)):
+            assert form(ok, good)[2:4] == [ok.data_ptr(), good.data_ptr()]
+        for bad in (_Cuda.of(2, 2, 64), _Cuda.of(3, 1, 64), _Cuda.of(3, 2, 64, dtype=torch.float32)):
+            for key, value in ((bad, good), (good, bad)):
+                with pytest.raises(ValueError):
+                    form(key, value)
+    assert forms[2](None, None)[2:4] == [None, None]
