@@ -544,8 +544,8 @@ def fp8_pool_shape(num_blocks, num_kv_heads, head_dim, block_size):
     return (num_blocks, num_kv_heads, head_dim // 16, block_size, 16)
 
 
-def _scale_ptr(t, name):
-    if t.dtype != torch.float32:
+def _scale_ptr(t, name, num_kv_heads):
+    if t.dtype != torch.float32 or t.numel() < num_kv_heads:
         raise ValueError(f"{name} must be float32 [num_kv_heads]")
     return _dev_ptr(t, name)
 
@@ -560,15 +560,16 @@ def pa_reshape_and_cache_fp8(key, value, k_cache, v_cache, slot_mapping, k_scale
     n, hkv, d, b = _pool_dims(k_cache)
     _check(lib.pa_reshape_and_cache_fp8(
         _dev_ptr(key, "key"), _dev_ptr(value, "value"), _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
-        _dev_ptr(slot_mapping, "slot_mapping"), _scale_ptr(k_scale, "k_scale"), _scale_ptr(v_scale, "v_scale"),
-        key.shape[0], hkv, d, b, n, _DTYPE[key.dtype], _stream(stream)), "pa_reshape_and_cache_fp8")
+        _dev_ptr(slot_mapping, "slot_mapping"), _scale_ptr(k_scale, "k_scale", hkv),
+        _scale_ptr(v_scale, "v_scale", hkv), key.shape[0], hkv, d, b, n, _DTYPE[key.dtype], _stream(stream)), "pa_reshape_and_cache_fp8")
 
 
 def _fp8_args(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, max_context_len):
     if k_cache.dtype != torch.uint8:
         raise ValueError("8-bit pools are uint8 tensors")
     a = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len)
-    return a[:4] + [_scale_ptr(k_scale, "k_scale"), _scale_ptr(v_scale, "v_scale")] + a[4:]
+    hkv = k_cache.shape[1]
+    return a[:4] + [_scale_ptr(k_scale, "k_scale", hkv), _scale_ptr(v_scale, "v_scale", hkv)] + a[4:]
 
 
 @_on_tensor_device

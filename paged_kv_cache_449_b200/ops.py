@@ -123,7 +123,7 @@ def _rope_args(pool, q_out, q, key, value, k_cache, v_cache, k_scale, v_scale, p
     qp, qs = _token_rows(q, "q")
     kp, ks = _token_rows(key, "key", hkv, D)
     vp, vs = _token_rows(value, "value", hkv, D)
-    scales = [_scale_ptr(k_scale, "k_scale"), _scale_ptr(v_scale, "v_scale")] if pool == "fp8" else []
+    scales = [_scale_ptr(k_scale, "k_scale", hkv), _scale_ptr(v_scale, "v_scale", hkv)] if pool == "fp8" else []
     return [_dev_ptr(q_out, "q_out"), qp, kp, vp, _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
             *scales, _per_token(positions, T, "positions"), _per_token(slot_mapping, T, "slot_mapping"),
             None if inv_freq is None else _dev_ptr(inv_freq, "inv_freq"),
@@ -384,6 +384,8 @@ def _decode_window_args(out, q, key, value, k_cache, v_cache, k_scale, v_scale, 
             raise ValueError("the pools share q's dtype")
         args = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len)
     else:
+        if v_cache.dtype != k_cache.dtype:
+            raise ValueError("8-bit pools are uint8 tensors")
         args = _fp8_args(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
                          max_context_len)
     cap = min(args[-3], int(block_tables.shape[1]) * b)

@@ -265,3 +265,28 @@ def test_append_rows_of_the_plain_decodes(lib):
                 with pytest.raises(ValueError):
                     form(key, value)
     assert forms[2](None, None)[2:4] == [None, None]
+
+
+def test_8_bit_scales_are_one_per_kv_head(lib):
+    """A scale is read for every kv head of the pools."""
+    q, i32, f32 = _Cuda.of(3, 4, 64), dict(dtype=torch.int32), dict(dtype=torch.float32)
+    rows, slots, freq = _Cuda.of(3, 2, 64), _Cuda.of(3, dtype=torch.int64), _Cuda.of(32, **f32)
+    pool = _Cuda.of(*pa.fp8_pool_shape(5, 2, 64, 16), dtype=torch.uint8)
+    tables, lens = _Cuda.of(3, 7, **i32), _Cuda.of(3, **i32)
+    forms = [lambda k, v: ops._decode_window_args(q, q, None, None, pool, pool, k, v, tables, lens, 0.125, 10, 0, None, 0,
+                                                  None, None, None, None),
+             lambda k, v: ops._rope_args("fp8", q, q, rows, rows, pool, pool, k, v, slots, slots, freq, False, 1.0, None,
+                                         None, 1e-6),
+             lambda k, v: pa._fp8_args(q, q, pool, pool, k, v, tables, lens, 0.125, None),
+             lambda k, v: pa.pa_reshape_and_cache_fp8.__wrapped__(rows[:0], rows[:0], pool, pool, slots[:0], k, v, stream=0)]
+    good = _Cuda.of(2, **f32)
+    for form in forms:
+        form(good, good)
+        for bad in (_Cuda.of(1, **f32), _Cuda.of(2, dtype=torch.float64)):
+            for k, v in ((bad, good), (good, bad)):
+                with pytest.raises(ValueError, match="scale"):
+                    form(k, v)
+    # ... and the windowed form's pools are both of bytes
+    with pytest.raises(ValueError):
+        ops._decode_window_args(q, q, None, None, pool, pool.half(), good, good, tables, lens, 0.125, 10, 0, None, 0, None,
+                                None, None, None)
