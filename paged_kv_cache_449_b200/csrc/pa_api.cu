@@ -635,13 +635,17 @@ __global__ void pa_test_wait_kernel(unsigned long long limit_ns, long long* elap
 
 }  // namespace
 
+// The hooks of the other translation unit (pa_ops.cu).
+extern "C" __attribute__((visibility("hidden"))) cudaError_t pa_ops_set_hooks(unsigned long long limit_ns,
+                                                                             int skip_first_copy);
+
 extern "C" pa_status pa_test_set_hooks(int64_t wait_limit_ns, int skip_first_copy) {
     if (wait_limit_ns <= 0) return PA_ERR_INVALID_ARG;
     const unsigned long long limit = static_cast<unsigned long long>(wait_limit_ns);
     if (cudaMemcpyToSymbol(pa::g_test_wait_limit_ns, &limit, sizeof(limit)) != cudaSuccess) return PA_ERR_CUDA;
     if (cudaMemcpyToSymbol(pa::g_test_skip_first_copy, &skip_first_copy, sizeof(int)) != cudaSuccess)
         return PA_ERR_CUDA;
-    return PA_OK;
+    return pa_ops_set_hooks(limit, skip_first_copy) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 extern "C" pa_status pa_test_wait_timeout(int64_t limit_ns, int64_t* elapsed_ns, void* stream) {

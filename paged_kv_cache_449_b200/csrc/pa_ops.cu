@@ -498,3 +498,12 @@ extern "C" __attribute__((visibility("hidden"))) cudaError_t pa_ops_take_error(i
     if (e == cudaSuccess && *value != 0) e = cudaMemcpyToSymbol(pa::g_device_error, &zero, sizeof(int));
     return e;
 }
+
+#ifdef PA_TEST_HOOKS
+// This unit's copies of the test hooks (pa_test_set_hooks sets both units').
+extern "C" __attribute__((visibility("hidden"))) cudaError_t pa_ops_set_hooks(unsigned long long limit_ns,
+                                                                             int skip_first_copy) {
+    const cudaError_t e = cudaMemcpyToSymbol(pa::g_test_wait_limit_ns, &limit_ns, sizeof(limit_ns));
+    return e != cudaSuccess ? e : cudaMemcpyToSymbol(pa::g_test_skip_first_copy, &skip_first_copy, sizeof(int));
+}
+#endif  // PA_TEST_HOOKS
