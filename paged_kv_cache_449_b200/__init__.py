@@ -522,6 +522,9 @@ def pa_copy_blocks(dst_k_cache, dst_v_cache, src_k_cache, src_v_cache, block_map
     byte pools of the 8- and 4-bit caches."""
     lib = load()
     if all(t.dtype == torch.uint8 for t in (dst_k_cache, dst_v_cache, src_k_cache, src_v_cache)):
+        if dst_k_cache.shape != dst_v_cache.shape or src_k_cache.shape != src_v_cache.shape or \
+                dst_k_cache.shape[1:] != src_k_cache.shape[1:]:
+            raise ValueError("source and destination pools differ in shape, or K's from V's")
         dst_k_cache, dst_v_cache, src_k_cache, src_v_cache = (
             _bytes_as_pool(t) for t in (dst_k_cache, dst_v_cache, src_k_cache, src_v_cache))
     n_src, hkv, d, b = _pool_dims(src_k_cache)

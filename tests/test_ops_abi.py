@@ -290,3 +290,21 @@ def test_8_bit_scales_are_one_per_kv_head(lib):
     with pytest.raises(ValueError):
         ops._decode_window_args(q, q, None, None, pool, pool.half(), good, good, tables, lens, 0.125, 10, 0, None, 0, None,
                                 None, None, None)
+
+
+def test_byte_pools_are_copied_between_pools_of_one_shape(lib):
+    """The sizes of a copy are read off one pool of a pair: the others have them too."""
+    def copy(*pools):
+        pairs = _Cuda.of(0, 2, dtype=torch.int64)
+        return pa.pa_copy_blocks.__wrapped__(*pools, pairs, stream=0)
+
+    u8 = dict(dtype=torch.uint8)
+    four, fewer = _Cuda.of(*ops.int4_pool_shape(6, 2, 64, 16), **u8), _Cuda.of(*ops.int4_pool_shape(4, 2, 64, 16), **u8)
+    eight, turned = _Cuda.of(*pa.fp8_pool_shape(6, 2, 64, 16), **u8), _Cuda.of(*pa.fp8_pool_shape(6, 2, 128, 8), **u8)
+    copy(four, four, fewer, fewer)      # swap-out: pools of other lengths
+    copy(eight, eight, eight, eight)
+    for pools in ((four, fewer, four, four), (four, four, four, fewer), (fewer, fewer, four, fewer),
+                  (eight, eight, turned, turned), (eight, turned, eight, eight),
+                  (four, four, _Cuda.of(*ops.int4_pool_shape(6, 1, 64, 32), **u8), _Cuda.of(*ops.int4_pool_shape(6, 1, 64, 32), **u8))):
+        with pytest.raises(ValueError, match="shape"):
+            copy(*pools)
