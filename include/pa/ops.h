@@ -113,6 +113,10 @@ pa_status pa_gather_cache_int4(void* key, void* value, const void* k_cache, cons
  * num_sinks.  Blocks that hold no such token are not read, and their
  * block-table entries may hold anything; the others' tokens that no query of the
  * sequence sees do not count, whatever the pool holds there.
+ * Scores, softmax and sums are fp32 as in pa.h.  For the product with V the
+ * tensor cores take each weight rounded to the pools' 16-bit type, as in
+ * pa_decode and pa_prefill (8-bit pools: to fp16; fp32 pools: not at all); in
+ * one pass, a window that reaches past the context gives the same bits as they do.
  *
  * The decode entries below share a plan:
  *   partition_size  0: one thread block per (sequence, kv head); otherwise the
@@ -164,7 +168,8 @@ pa_status pa_decode_window_fp8(void* out, const void* q, const void* key, const 
  * window.  The codes are multiplied as whole numbers, scales and zeros applied
  * in fp32; each head's query (|q| < 2^114) is scaled by a power of two into
  * fp16's range first, exactly (elements below 2^-23 of the head's largest keep
- * 2^-34 of it).
+ * 2^-34 of it).  A weight times its token's scale of V is rounded to fp16 (2^-11,
+ * or 2^-30 of the largest weight times the context's largest scale).
  */
 pa_status pa_decode_int4(void* out, const void* q, const void* k_cache, const void* v_cache,
                          const int32_t* block_tables, const int32_t* context_lens, float scale, int block_size,

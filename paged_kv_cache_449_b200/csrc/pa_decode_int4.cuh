@@ -43,9 +43,12 @@
 //
 // Statistics: fp32 running reference and sum in base 2.  The reference moves
 // only when a score exceeds it by 2^8 (one vote a unit instead of a reduction
-// and a rescale).  p * scale of V is rounded to fp16 for the product, within
+// and a rescale).  p * scale of V is rounded to fp16 for the product (2^-11,
+// where fp32 would take a second product for the remainder), within
 // the range of fp16 whatever the scales are: they are taken relative to a
 // power of two that moves, like the reference, when a larger scale appears.
+// The largest scale lies in [2^5, 2^7) then, so a weight keeps its 11 bits
+// down to 2^-19 of it, and below that 2^-30 of the largest scale.
 #pragma once
 
 #include "pa_decode.cuh"
@@ -135,7 +138,7 @@ struct VisibleSteps {
 };
 
 // Warps an SM holds.  D = 128: 12 of 160 registers (one pass over 64 sequences
-// 30.6 us, the 70B long batch 142 us) rather than 16 of 128 (32.7 and 150 us).
+// 29.9 us, the 70B long batch 151 us) rather than 16 of 128 (34.9 and 152 us).
 template <int D>
 constexpr int kInt4Resident = D == 128 ? 12 : 16;
 template <int D, int B, int NW, int ST>

@@ -44,7 +44,7 @@ int choose_deep_partition(long long pairs, long long units, int unit) {
 }
 
 // 4-bit pools: the same while the SMs hold the (sequence, kv head) pairs twice
-// (one 32k sequence of 8 heads: 15.8 us, 19.5 in wide blocks of 1024 tokens) or
+// (one 32k sequence of 8 heads: 15.9 us, 19.5 in wide blocks of 1024 tokens) or
 // contexts are short; beyond, partitions for wide blocks: 2048 tokens (one's
 // start and merge cost as much as 100 tokens a warp), more where that would be
 // over 16 an SM.

@@ -843,7 +843,12 @@ __global__ void __launch_bounds__((6 * QT + 2) * 32, QT == 2 ? 1 : 2) pa_prefill
             uint64_t acc[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[e] = tc::f2(0.f, 0.f);
-            uint32_t pw[kKeys / 2];   // P row, 16-bit pairs: the A-operand columns of O += P V
+            // P row, 16-bit pairs: the A-operand columns of O += P V.  Rounded to
+            // V's type (kind::f16 takes both operands in one): u a weight at
+            // most; the row sums are of the unrounded weights.  (A bf16 window of
+            // 1024: 2.3e-3 from the exact output, where rounding the output alone
+            // gives 1.7e-3.)
+            uint32_t pw[kKeys / 2];
 #pragma unroll
             for (int k8 = 0; k8 < kKeys / 8; ++k8) {
 #pragma unroll
