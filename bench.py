@@ -147,20 +147,20 @@ def make_workload(name, seed, device, block_size=None):
 # in profiles/).  Keyed by a hash of the kernel sources: once the kernels change,
 # the figure no longer describes them and the bench reports null.
 NCU_TRAFFIC = {
-    "9370882dc6352751": {
+    "0bb114f81073fe3d": {
         ("llama3_8b_decode_bf16", "append"): 292.756e6 + 3.271e6,
         ("continuous_batching_mix_bf16_B16", "append"): 211.593e6 + 3.144e6,
         ("llama3_70b_long_bf16", "splitk"): 2.519479e9 + 6.995e6,
         ("llama3_8b_decode_bf16+e4m3", "append"): 146.831e6 + 3.136e6,
         ("llama3_70b_long_bf16+e4m3", "splitk"): 1.260221e9 + 6.095e6,
     },
-    "cb5adfbd98df0306": {
+    "c6663066924328e0": {
         ("chunked_prefill_bfloat16", "prefill"): 118.627e6 + 19.799e6,
         ("chunked_prefill_bfloat16_B8", "prefill"): 118.360e6 + 19.872e6,
         ("chunked_prefill_bfloat16_B32", "prefill"): 118.734e6 + 20.706e6,
     },
     # the shared-prefix step: its prefix pass plus its decode pass
-    "575f84905104d681": {
+    "b2b5b164c2a17192": {
         ("prefix_sharing_f16_p1024", "shared_prefix"): 5.319e6 + 0.0 + 153.340e6 + 0.276e6,
     },
 }
