@@ -268,18 +268,20 @@ def _partials(need, workspace, counters, num_counters, device, lasting):
     two tensors, and those of them that were made here because they were not
     given, for this call alone (calls that overlap may not share them).
     `lasting`: they outlive this call.  What a capture makes is zeroed by the
-    graph's replays, not now, so counters that outlive the captured call (a
-    handle's, a Counters') are not made while the stream is capturing."""
+    graph's replays, not now, so a handle's counters are not made while the
+    stream is capturing, and a Counters does not grow then (the captured call
+    has counters of its own)."""
     if need == 0:
         return [None, 0, None, 0], (), ()
     made = ()
     if isinstance(counters, Counters):
-        missing = counters.buf is None or counters.buf.numel() < num_counters or counters.buf.device != device
-    else:
-        missing = counters is None and lasting
-    if missing and torch.cuda.is_current_stream_capturing():
-        raise ValueError("counters that outlive the call cannot be made while the stream is capturing: prepare the "
-                         "call before the capture, or give zeroed counters")
+        had = counters.buf
+        if (had is None or had.numel() < num_counters or had.device != device) and \
+                torch.cuda.is_current_stream_capturing():
+            counters = None
+    if counters is None and lasting and torch.cuda.is_current_stream_capturing():
+        raise ValueError("a handle's counters cannot be made while the stream is capturing: prepare the call before "
+                         "the capture, or give zeroed counters")
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
         made += (workspace,)
@@ -288,7 +290,6 @@ def _partials(need, workspace, counters, num_counters, device, lasting):
         made += (counters,)
     buf = counters
     if isinstance(counters, Counters):
-        had = counters.buf
         buf = counters.get(num_counters, device)
         if buf is not had:
             made += (buf,)

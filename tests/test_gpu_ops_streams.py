@@ -91,7 +91,8 @@ def test_a_handle_is_not_made_in_a_capture(setting, kind):
     caller's, or made before, its captured calls are the eager ones."""
     calls, base = setting
     fn, prepare, args, kw = calls[kind]
-    outs = [torch.zeros_like(base[kind]) for _ in range(3)]
+    outs = [torch.zeros_like(base[kind]) for _ in range(4)]
+    kept = pa.Counters()
     counters = torch.zeros(2, dtype=torch.int32, device="cuda")
     before = prepare(*args(outs[0]), partition_size=64, **kw)
     graph = torch.cuda.CUDAGraph()
@@ -99,14 +100,16 @@ def test_a_handle_is_not_made_in_a_capture(setting, kind):
         with pytest.raises(ValueError, match="capturing"):
             prepare(*args(outs[0]), partition_size=64, **kw)
         with pytest.raises(ValueError, match="capturing"):
-            fn(*args(outs[0]), partition_size=64, counters=pa.Counters(), **kw)
+            prepare(*args(outs[0]), partition_size=64, counters=kept, **kw)
         before()
         given = prepare(*args(outs[1]), partition_size=64, counters=counters, **kw)
         given()
         fn(*args(outs[2]), partition_size=64, **kw)     # buffers of its own, in the graph
+        fn(*args(outs[3]), partition_size=64, counters=kept, **kw)     # as well: a Counters does not grow there
     given()
+    fn(*args(outs[3]), partition_size=64, counters=kept, **kw)         # eagerly, before any replay
     torch.cuda.synchronize()
-    assert torch.equal(outs[1], base[kind])
+    assert torch.equal(outs[1], base[kind]) and torch.equal(outs[3], base[kind])
     for _ in range(2):
         for out in outs:
             out.zero_()

@@ -115,18 +115,20 @@ def test_only_buffers_made_for_a_handle_are_waited_for(monkeypatch):
 
 
 def test_counters_that_outlive_a_captured_call_are_not_made_in_the_capture(monkeypatch):
-    """They would be zeroed by the graph's replays only."""
+    """They would be zeroed by the graph's replays only: a handle refuses, and a
+    Counters that is too small stays as it is (the call has its own)."""
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    monkeypatch.setattr(ops, "_dev_ptr", lambda t, name: t.data_ptr())
     cpu, workspace = torch.device("cpu"), Held.of(torch.zeros(256, dtype=torch.uint8))
     with pytest.raises(ValueError, match="capturing"):
         ops._partials(256, workspace, None, 8, cpu, True)
     small = pa.Counters()
-    for lasting in (True, False):
-        for buf in (None, Held.of(torch.zeros(7, dtype=torch.int32))):
-            small.buf = buf
-            with pytest.raises(ValueError, match="capturing"):
-                ops._partials(256, workspace, small, 8, cpu, lasting)
-    assert small.buf.numel() == 7
+    for buf in (None, Held.of(torch.zeros(7, dtype=torch.int32))):
+        small.buf = buf
+        with pytest.raises(ValueError, match="capturing"):
+            ops._partials(256, workspace, small, 8, cpu, True)
+        args, held, made = ops._partials(256, workspace, small, 8, cpu, False)
+        assert small.buf is buf and held[1] is made[0] and held[1].numel() == 8 and args[2] == held[1].data_ptr()
     # given, large enough, or not needed
     given = Held.of(torch.zeros(8, dtype=torch.int32))
     small.buf, small.get = given, lambda n, device: given
